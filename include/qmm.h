@@ -293,6 +293,76 @@ int qmm_actorder(const void* x, int xdtype, const int32_t* perm, const void* qwe
                  int bits, int group, int mode, void* y, void* workspace, size_t workspace_bytes,
                  void* stream);
 
+/* ---- 4-bit key / value cache, and attention over it.  (Additions of this
+ * library: a decoder layer that streams its weights in 4 bits reads its cache
+ * once per token too.)
+ *
+ * The cache is pages of `page` tokens (a power of two >= 16), each holding the
+ * keys and values of `heads` heads of `dim` values (64, 128 or 256) as 4-bit
+ * codes with one fp16 scale per token, head and group of `group` dims (-1: the
+ * whole row; or a power of two >= 32 up to dim), in one buffer the caller owns
+ * (qmm_kv_cache_size bytes, 16-byte aligned):
+ *   QMM_SYM   (q - 8) s    s = absmax / 7,     q = clamp(rint(x / s) + 8, 0, 15)
+ *   QMM_ASYM  (q - z) s    s = (hi - lo) / 15, z = clamp(rint(-lo / s), 0, 15),
+ *                          q = clamp(rint(x / s) + z, 0, 15), with lo = min(x, 0),
+ *                          hi = max(x, 0): nothing is clipped
+ * with the arithmetic of qmm_pack (IEEE fp32, s rounded to fp16 first, half to
+ * even).  s saturates at 4096, so that every stored value is finite in fp16; a
+ * group whose fp16 scale is 0 encodes zeros; a NaN encodes as 0, an infinity as
+ * the largest code.
+ * A slot is page * `page` + the place in the page.
+ *
+ * Layout: [pages][heads][page / 16] tiles of 16 tokens; a tile holds key codes
+ * [16][dim / 2], value codes [16][dim / 2], key parameters [16][G], value
+ * parameters [16][G] (G = dim / group; a parameter is the fp16 scale, in
+ * QMM_ASYM the fp16 pair (s, z)).  A code row is dim / 8 little-endian words of
+ * eight consecutive dims, nibble i the i-th.  Word n of a key row stands at word
+ * 4 p + (n / 4) % 4 with p = n % 4 + 4 (n / 16), p xor 4 (token % 2) for dim 256
+ * (dim 64: at 2 (n % 4) + n / 4).  A value row is eight pieces of dim / 16 bytes;
+ * piece i stands at i xor 4 ((token / 2) % 2) for dim 128, i xor 2 (token % 4) for
+ * dim 256, i for dim 64.  The order is the one the attention kernel reads
+ * without bank conflicts.
+ *
+ * qmm_kv_store quantizes the rows k[i], v[i] (device, [tokens][heads][dim],
+ * dtype fp16 or bf16; k_stride / v_stride elements between tokens, multiples of
+ * 8, rows 16-byte aligned) into slots[i] (device, int32).  A slot outside the
+ * cache (negative: padding) is skipped.  The slots of a call must differ.
+ * qmm_kv_load decodes slots[i] into k[i], v[i] (contiguous [tokens][heads][dim]),
+ * (q - z) s rounded once; a slot outside the cache gives zeros. */
+size_t qmm_kv_cache_size(int pages, int heads, int dim, int page, int group, int mode);
+int qmm_kv_store(const void* k, const void* v, int dtype, long long k_stride, long long v_stride,
+                 const int32_t* slots, int tokens, int heads, int dim, int page, int pages, int group,
+                 int mode, void* cache, void* stream);
+int qmm_kv_load(const void* cache, const int32_t* slots, int tokens, int heads, int dim, int page, int pages,
+                int group, int mode, int dtype, void* k, void* v, void* stream);
+
+/* Attention of each sequence's last tokens over its cache:
+ *   out[i, h] = sum_t softmax_t(scale q[i, h] . k~[t, h'])  v~[t, h'],  h' = h / (q_heads / kv_heads)
+ * Sequence b has lens[b] tokens in the pages table[b][0 ..] (device, int32
+ * [batch][max_pages]) and the queries cu_q[b] .. cu_q[b + 1] - 1 (device, int32
+ * [batch + 1]), which are its last tokens: a query sees the tokens up to its own
+ * (store a step's keys and values first), with window > 0 only the last `window`
+ * of them.  cu_q NULL: one query per sequence (total_q = batch, max_q = 1).
+ *   q     [total_q][q_heads][dim], out the same (strides as for k; no overlap)
+ *   max_q an upper bound on the queries of a sequence; those past it get no output
+ *   lse   fp32 [total_q][q_heads], log of the sum of exponentials, or NULL
+ * A query that sees nothing (an empty sequence) gives zeros and lse -inf.  Rows of
+ * out past cu_q[batch] are left as they are.  Lengths and pages are read on the
+ * device, so a captured graph serves new ones; lengths are clamped to max_pages
+ * pages, query ranges to total_q, and a page outside the cache reads as page 0 (no
+ * access outside the buffers).  Nothing stored past a sequence's length or before
+ * its window is used.  The sums, the softmax and its statistics are fp32; keys
+ * enter exactly, values and probabilities with one fp16 rounding each.
+ * workspace: qmm_kv_workspace_size bytes, 256-byte aligned, under the rules of
+ * qmm's (zero filled once, reusable on a stream, one per concurrent call); NULL:
+ * no tile of rows is split between CTAs (slower for few, long sequences). */
+size_t qmm_kv_workspace_size(int batch, int max_q, int q_heads, int kv_heads, int dim);
+int qmm_kv_attend(const void* q, int dtype, long long q_stride, const void* cache, const int32_t* table,
+                  const int32_t* lens, const int32_t* cu_q, int batch, int total_q, int max_q, int q_heads,
+                  int kv_heads, int dim, int page, int pages, int max_pages, int group, int mode, float scale,
+                  int window, void* out, long long out_stride, float* lse, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
 /* Decode the packed weights into W_out[N, K] row-major (fp16 or bf16 by
  * out_dtype): W_out = round_to_nearest_even((q - z) * s) (SYM z = 8) or
  * round(T[q] * s), the product taken exactly in fp32 (exact for integer

@@ -32,7 +32,8 @@ SYMBOLS = ("qmm_packed_size", "qmm_pack", "qmm_workspace_size", "qmm_workspace_s
            "qmm_pack_gated", "qmm_gated", "qmm_zeros_size", "qmm_pack_asym",
            "qmm_workspace_size_asym", "qmm_asym", "qmm_dequant_asym", "qmm_actorder_perm",
            "qmm_pack_actorder", "qmm_workspace_size_actorder", "qmm_actorder",
-           "qmm_set_wait_limit")
+           "qmm_set_wait_limit", "qmm_kv_cache_size", "qmm_kv_store", "qmm_kv_load",
+           "qmm_kv_workspace_size", "qmm_kv_attend")
 
 _lib = None
 _lock = threading.Lock()
@@ -81,6 +82,15 @@ def load(path: str = LIB_PATH):
             lib.qmm_workspace_size_actorder.argtypes = [I, I, I, I, I, I]
             lib.qmm_workspace_size_actorder.restype = S
             lib.qmm_actorder.argtypes = [P, I, P, P, P, P, I, I, I, I, I, I, P, P, S, P]
+            L, F = ctypes.c_longlong, ctypes.c_float
+            lib.qmm_kv_cache_size.argtypes = [I, I, I, I, I, I]
+            lib.qmm_kv_cache_size.restype = S
+            lib.qmm_kv_store.argtypes = [P, P, I, L, L, P, I, I, I, I, I, I, I, P, P]
+            lib.qmm_kv_load.argtypes = [P, P, I, I, I, I, I, I, I, I, P, P, P]
+            lib.qmm_kv_workspace_size.argtypes = [I, I, I, I, I]
+            lib.qmm_kv_workspace_size.restype = S
+            lib.qmm_kv_attend.argtypes = [P, I, L, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, F, I,
+                                          P, L, P, P, S, P]
             lib.qmm_check_error.argtypes = [P]
             lib.qmm_set_wait_limit.argtypes = [ctypes.c_longlong]
             lib.qmm_set_wait_limit.restype = ctypes.c_longlong
@@ -361,6 +371,136 @@ def qmm_actorder(x, perm, qweight, scales, zeros_or_lut, N, K, mode, bits=4, gro
                                _ptr(zeros_or_lut), M, N, K, bits, group, MODES[mode], _ptr(y),
                                _ptr(ws), nbytes, _stream()), "qmm_actorder")
     return y
+
+
+# ---- 4-bit key / value cache and attention over it
+
+def _here(name, t, *dtypes):
+    """t is on the current device and of one of the dtypes (its kernel runs there)."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if dtypes and t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}")
+
+
+def _token_rows(name, t, *dtypes):
+    """t is [tokens, heads, dim] with contiguous rows of heads: (heads, dim, token stride)."""
+    _here(name, t, *dtypes)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim]")
+    T, H, D = t.shape
+    if T > 0 and ((D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    # a single token's stride says nothing
+    return H, D, t.stride(0) if T > 1 else H * D
+
+
+def _int_vector(name, t, n=None):
+    _here(name, t, torch.int32)
+    if t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be a contiguous int32 vector" + ("" if n is None else f" of {n}"))
+
+
+def _cache_shape(cache, dim, mode, group):
+    """(pages, heads, page) of a kv_cache() tensor of this format."""
+    _here("cache", cache, torch.uint8)
+    if cache.dim() != 4 or not cache.is_contiguous():
+        raise ValueError("cache must be a tensor of kv_cache()")
+    pages, heads, tiles, nbytes = cache.shape
+    want = load().qmm_kv_cache_size(pages, heads, dim, 16 * tiles, group, MODES[mode])
+    if want == 0:
+        raise QmmError(-2, "qmm_kv_cache_size")
+    if want != cache.numel():
+        raise ValueError(f"cache: tiles of {nbytes} bytes do not hold dim {dim}, {mode}, group {group}")
+    return pages, heads, 16 * tiles
+
+
+def kv_cache(pages, heads, dim, page=64, mode="sym", group=-1, device="cuda"):
+    """A zero-filled 4-bit cache: uint8 [pages, heads, page / 16, bytes of a 16-token tile]."""
+    n = load().qmm_kv_cache_size(pages, heads, dim, page, group, MODES[mode])
+    if n == 0:
+        raise QmmError(-2, "qmm_kv_cache_size")
+    return torch.zeros(pages, heads, page // 16, n // (pages * heads * (page // 16)), dtype=torch.uint8,
+                       device=device)
+
+
+def kv_store(k, v, slots, cache, mode="sym", group=-1):
+    """Quantize k[i], v[i] ([tokens, heads, dim], fp16 or bf16; slices of a fused
+    projection are taken as they are) into slots[i] (int32: page index times the
+    page length + place; negative: skipped) of the cache."""
+    H, D, ks = _token_rows("k", k, *DTYPES)
+    Hv, Dv, vs = _token_rows("v", v, k.dtype)
+    if (k.shape[0], H, D) != (v.shape[0], Hv, Dv):
+        raise ValueError("k and v must have the same shape")
+    _int_vector("slots", slots, k.shape[0])
+    pages, heads, page = _cache_shape(cache, D, mode, group)
+    if heads != H:
+        raise ValueError(f"the cache holds {heads} heads, k has {H}")
+    _check(load().qmm_kv_store(_ptr(k), _ptr(v), DTYPES[k.dtype], ks, vs, _ptr(slots), k.shape[0], H, D,
+                               page, pages, group, MODES[mode], _ptr(cache), _stream()), "qmm_kv_store")
+
+
+def kv_load(cache, slots, dim, mode="sym", group=-1, dtype=torch.float16, out=None):
+    """The decoded keys and values ([tokens, heads, dim] each) of the given slots."""
+    _int_vector("slots", slots)
+    pages, heads, page = _cache_shape(cache, dim, mode, group)
+    shape = (slots.shape[0], heads, dim)
+    if out is None:
+        out = tuple(torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
+    k, v = out
+    for name, t in (("k", k), ("v", v)):
+        _here(name, t, *DTYPES)
+        if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype != k.dtype:
+            raise ValueError(f"{name} must be a contiguous {list(shape)} tensor")
+    _check(load().qmm_kv_load(_ptr(cache), _ptr(slots), shape[0], heads, dim, page, pages, group, MODES[mode],
+                              DTYPES[k.dtype], _ptr(k), _ptr(v), _stream()), "qmm_kv_load")
+    return k, v
+
+
+def kv_workspace(batch, max_q, q_heads, kv_heads, dim, device="cuda"):
+    """A zero-filled workspace for kv_attend calls of up to these sizes' shape
+    (one per shape and stream, reusable)."""
+    n = load().qmm_kv_workspace_size(batch, max_q, q_heads, kv_heads, dim)
+    if n == 0:
+        raise QmmError(-2, "qmm_kv_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def kv_attend(q, cache, table, lens, cu_q=None, max_q=1, scale=None, window=0, mode="sym", group=-1,
+              out=None, lse=None, ws=None):
+    """Attention of each sequence's last tokens, q [total, heads, dim], over its
+    pages of the cache: sequence b has lens[b] tokens in pages table[b] and the
+    queries cu_q[b] .. cu_q[b + 1] - 1 (None: one each), at most max_q of them.
+
+    scale: None for 1 / sqrt(dim); window: 0, or how many last tokens a query
+    sees; lse: fp32 [total, heads] to fill with the log-sum-exp; ws: a
+    kv_workspace() (split over all SMs), or None."""
+    H, D, qstride = _token_rows("q", q, *DTYPES)
+    pages, kvh, page = _cache_shape(cache, D, mode, group)
+    _here("table", table, torch.int32)
+    if table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table must be a contiguous int32 [batch, pages] tensor")
+    B, total = table.shape[0], q.shape[0]
+    _int_vector("lens", lens, B)
+    if cu_q is not None:
+        _int_vector("cu_q", cu_q, B + 1)
+    if out is None:
+        out = torch.empty(total, H, D, dtype=q.dtype, device=q.device)
+    Ho, Do, ostride = _token_rows("out", out, q.dtype)
+    if (out.shape[0], Ho, Do) != (total, H, D):
+        raise ValueError("out must have q's shape")
+    if lse is not None:
+        _here("lse", lse, torch.float32)
+        if tuple(lse.shape) != (total, H) or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous fp32 [total, heads] tensor")
+    if ws is not None:
+        _here("ws", ws)
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(load().qmm_kv_attend(_ptr(q), DTYPES[q.dtype], qstride, _ptr(cache), _ptr(table), _ptr(lens),
+                                _ptr(cu_q), B, total, max_q, H, kvh, D, page, pages, table.shape[1], group,
+                                MODES[mode], D ** -0.5 if scale is None else scale, window, _ptr(out), ostride,
+                                _ptr(lse), _ptr(ws), nbytes, _stream()), "qmm_kv_attend")
+    return out
 
 
 def check_error():

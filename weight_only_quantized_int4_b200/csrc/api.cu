@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "kv.cuh"
 
 namespace qk {
 
@@ -65,6 +66,27 @@ void zero_mode(int K, int group, int zgroup, int zbits, int* mode, int* zg) {
   const int L = group == -1 ? K : group, LZ = zgroup == -1 ? K : zgroup;
   *zg = LZ == L ? 0 : zgroup;
   *mode = zbits == 4 ? (LZ >= 128 ? kASYMQ1 : kASYMQ) : (*zg == 0 ? QMM_ASYM : kASYMX);
+}
+
+// The cache's format, checked; G groups of dims per row.
+int kv_format(int pages, int heads, int dim, int page, int group, int mode, KvCache* c) {
+  if (pages <= 0 || heads <= 0) return QMM_ERR_ARG;
+  if (mode != QMM_SYM && mode != QMM_ASYM && mode != QMM_LUT) return QMM_ERR_ARG;
+  if (mode == QMM_LUT) return QMM_ERR_UNSUPPORTED;
+  if (dim != 64 && dim != 128 && dim != 256) return QMM_ERR_UNSUPPORTED;
+  if (page < kKvTile || page > (1 << 16) || (page & (page - 1)) != 0) return QMM_ERR_UNSUPPORTED;
+  if (group != -1 && (group < 32 || (group & (group - 1)) != 0 || group > dim)) return QMM_ERR_UNSUPPORTED;
+  if (heads > 4096 || (long long)pages * page > (1ll << 31) - 1) return QMM_ERR_UNSUPPORTED;   // 32-bit slots
+  *c = KvCache{nullptr, pages, heads, dim, __builtin_ctz((unsigned)page), group == -1 ? 1 : dim / group, mode};
+  return QMM_OK;
+}
+
+int check_attend(int batch, int max_q, int q_heads, int kv_heads, int dim) {
+  if (batch <= 0 || max_q <= 0 || q_heads <= 0 || kv_heads <= 0) return QMM_ERR_ARG;
+  if (q_heads % kv_heads != 0) return QMM_ERR_ARG;
+  if (dim != 64 && dim != 128 && dim != 256) return QMM_ERR_UNSUPPORTED;
+  if (batch > (1 << 20) || max_q > (1 << 22) || q_heads > 4096) return QMM_ERR_UNSUPPORTED;   // 32-bit rows
+  return QMM_OK;
 }
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
@@ -420,6 +442,102 @@ int qmm_actorder(const void* x, int xdtype, const int32_t* perm, const void* qwe
   if (st != QMM_OK) return st;
   return run_qmm(xp, xdtype, qweight, scales, zeros_or_lut, M, N, K, bits, group, mode, y,
                  workspace, plain, stream, QMM_PATH_AUTO, false);
+}
+
+// ------------------------------------------------- 4-bit key / value cache
+
+size_t qmm_kv_cache_size(int pages, int heads, int dim, int page, int group, int mode) {
+  KvCache c;
+  if (kv_format(pages, heads, dim, page, group, mode, &c) != QMM_OK) return 0;
+  return (size_t)pages * heads * (page / kKvTile) * kv_tile_bytes(dim, c.G, mode);
+}
+
+int qmm_kv_store(const void* k, const void* v, int dtype, long long k_stride, long long v_stride,
+                 const int32_t* slots, int tokens, int heads, int dim, int page, int pages, int group,
+                 int mode, void* cache, void* stream) {
+  KvCache c;
+  int st = kv_format(pages, heads, dim, page, group, mode, &c);
+  if (st != QMM_OK) return st;
+  if (dtype != QMM_F16 && dtype != QMM_BF16) return QMM_ERR_ARG;
+  if (tokens < 0) return QMM_ERR_ARG;
+  if (tokens == 0) return QMM_OK;
+  if (!k || !v || !slots || !cache) return QMM_ERR_ARG;
+  const long long row = (long long)heads * dim;
+  if (k_stride < row || v_stride < row) return QMM_ERR_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned(slots, 4) ||
+      !aligned(cache, 16))
+    return QMM_ERR_ALIGN;
+  c.data = cache;
+  return status_of(launch_kv_store(c, k, v, dtype == QMM_BF16, k_stride, v_stride, slots, tokens,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+int qmm_kv_load(const void* cache, const int32_t* slots, int tokens, int heads, int dim, int page, int pages,
+                int group, int mode, int dtype, void* k, void* v, void* stream) {
+  KvCache c;
+  int st = kv_format(pages, heads, dim, page, group, mode, &c);
+  if (st != QMM_OK) return st;
+  if (dtype != QMM_F16 && dtype != QMM_BF16) return QMM_ERR_ARG;
+  if (tokens < 0) return QMM_ERR_ARG;
+  if (tokens == 0) return QMM_OK;
+  if (!k || !v || !slots || !cache) return QMM_ERR_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4) || !aligned(cache, 16)) return QMM_ERR_ALIGN;
+  c.data = const_cast<void*>(cache);
+  return status_of(launch_kv_load(c, slots, tokens, dtype == QMM_BF16, k, v, static_cast<cudaStream_t>(stream)));
+}
+
+size_t qmm_kv_workspace_size(int batch, int max_q, int q_heads, int kv_heads, int dim) {
+  if (check_attend(batch, max_q, q_heads, kv_heads, dim) != QMM_OK) return 0;
+  return kv_attend_workspace(batch, max_q, q_heads, kv_heads, dim, device_sms());
+}
+
+int qmm_kv_attend(const void* q, int dtype, long long q_stride, const void* cache, const int32_t* table,
+                  const int32_t* lens, const int32_t* cu_q, int batch, int total_q, int max_q, int q_heads,
+                  int kv_heads, int dim, int page, int pages, int max_pages, int group, int mode, float scale,
+                  int window, void* out, long long out_stride, float* lse, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  KvAttend p{};
+  int st = kv_format(pages, kv_heads, dim, page, group, mode, &p.cache);
+  if (st != QMM_OK) return st;
+  if (dtype != QMM_F16 && dtype != QMM_BF16) return QMM_ERR_ARG;
+  if (batch == 0 || total_q == 0) return batch < 0 || total_q < 0 ? QMM_ERR_ARG : QMM_OK;
+  st = check_attend(batch, max_q, q_heads, kv_heads, dim);
+  if (st != QMM_OK) return st;
+  if (total_q < 0 || max_pages <= 0 || window < 0 || !(scale == scale)) return QMM_ERR_ARG;
+  if (!cu_q && (total_q != batch || max_q != 1)) return QMM_ERR_ARG;   // one query per sequence
+  if ((long long)max_pages * page > (1ll << 30)) return QMM_ERR_UNSUPPORTED;   // 32-bit token positions
+  if (!q || !cache || !table || !lens || !out) return QMM_ERR_ARG;
+  const long long row = (long long)q_heads * dim;
+  if (q_stride < row || out_stride < row) return QMM_ERR_ARG;
+  if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(out, 16) || out_stride % 8 != 0 || !aligned(cache, 16) ||
+      !aligned(table, 4) || !aligned(lens, 4) || !aligned(cu_q, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
+    return QMM_ERR_ALIGN;
+  {
+    const char* qb = static_cast<const char*>(q);
+    const char* ob = static_cast<const char*>(out);
+    const size_t qs = ((size_t)(total_q - 1) * q_stride + row) * 2, os = ((size_t)(total_q - 1) * out_stride + row) * 2;
+    if (qb < ob + os && ob < qb + qs) return QMM_ERR_ARG;   // out overlaps q
+  }
+  if (workspace && workspace_bytes < kv_attend_workspace(batch, max_q, q_heads, kv_heads, dim, device_sms()))
+    return QMM_ERR_WORKSPACE;
+  p.cache.data = const_cast<void*>(cache);
+  p.q = q;
+  p.bf16 = dtype == QMM_BF16;
+  p.q_stride = q_stride;
+  p.out_stride = out_stride;
+  p.table = table;
+  p.lens = lens;
+  p.cu_q = cu_q;
+  p.batch = batch;
+  p.total_q = total_q;
+  p.max_q = max_q;
+  p.q_heads = q_heads;
+  p.max_pages = max_pages;
+  p.scale = scale;
+  p.window = std::min(window, 1 << 30);
+  p.out = out;
+  p.lse = lse;
+  return status_of(launch_kv_attend(p, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 long long qmm_set_wait_limit(long long cycles) {

@@ -83,6 +83,41 @@ cudaError_t launch_gidx_perm(const int* g_idx, int K, int group, int* perm, int*
 cudaError_t launch_permute_x(const void* x, const int* perm, int M, int K, void* xp,
                              cudaStream_t stream);
 
+// ---- 4-bit key / value cache (kv.cuh has the layout)
+
+// Largest group scale: (q - z) s with |q - z| <= 15 stays finite in fp16.
+constexpr float kKvMaxScale = 4096.0f;
+
+struct KvCache {
+  void* data;
+  int pages, heads, dim, page_log2, G, mode;   // G groups per row; mode kSYM or kASYM
+};
+
+cudaError_t launch_kv_store(const KvCache& c, const void* k, const void* v, bool bf16, long long k_stride,
+                            long long v_stride, const int* slots, int tokens, cudaStream_t stream);
+cudaError_t launch_kv_load(const KvCache& c, const int* slots, int tokens, bool bf16, void* k, void* v,
+                           cudaStream_t stream);
+
+// Attention over the cache.
+struct KvAttend {
+  KvCache cache;
+  const void* q;
+  bool bf16;
+  long long q_stride, out_stride;   // elements between tokens
+  const int* table;                 // [batch][max_pages]
+  const int* lens;                  // [batch]
+  const int* cu_q;                  // [batch + 1], or null: one query per sequence
+  int batch, total_q, max_q, q_heads, max_pages;
+  float scale;
+  int window;                       // 0: every earlier token
+  void* out;
+  float* lse;                       // [total_q][q_heads] or null
+};
+
+size_t kv_attend_workspace(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms);
+// workspace null: no tile is split between CTAs
+cudaError_t launch_kv_attend(const KvAttend& p, void* workspace, cudaStream_t stream);
+
 int device_sms();
 
 // cuTensorMapEncodeTiled from the driver (looked up once), or nullptr.

@@ -1,0 +1,803 @@
+// Attention of a few query rows per key head over the 4-bit cache.
+//
+//   o[i] = sum_t p[i, t] v~[t],  p[i, :] = softmax over the visible t of scale q[i] . k~[t]
+//
+// in one pass over the codes with a running maximum m and sum l per row:
+//   m' = max(m, x),  l' = l 2^(m - m') + 2^(x - m'),  o' = o 2^(m - m') + 2^(x - m') v~.
+//
+// The rows that share a key head (its query heads times their tokens) are the
+// N = 8 columns of m16n8k16 MMAs, so a key or value is decoded once for all of
+// them:
+//   S^T[16 tokens, 8 rows] = K~[16 tokens, D] . Q^T        A = decoded key codes
+//   O^T[D, 8 rows]        += V~^T[D, 16 tokens] . P^T      A = decoded value codes
+// S's accumulator fragment becomes P's operand fragment by one 8 x 8 transpose
+// in registers (movmatrix) per eight tokens.  Keys enter as the exact integers
+// q - z, their scale multiplies the fp32 sums (per group of dims); values enter
+// as fp16((q - z) s), one rounding of 2^-11; P is rounded to fp16 after a
+// factor of 2^15 that puts its range at 2^15 .. 2^-24, so a long tail of small
+// probabilities is not lost; S, m, l and O are fp32.  bf16 queries are moved to
+// fp16 by a power of two per row (exact down to 2^-28 of the row's largest).
+//
+// Work split: a tile is one (sequence, key head, RT query rows); it has ceil(
+// keys / kStepTok) steps.  The steps of all tiles are divided evenly over the
+// resident CTAs (their number comes from the lengths on the device, so a
+// captured graph serves any lengths).  Inside a CTA each warp takes 32 tokens
+// of a step through its own ring of cp.async stages; the warps' results meet
+// in shared memory.  A tile split between CTAs leaves fp32 partials in the
+// workspace, and the last CTA to arrive adds them in order.  No CTA waits for
+// another.
+#include <algorithm>
+
+#include "kv.cuh"
+
+namespace qk {
+namespace {
+
+constexpr int kAtWarps = 4;
+constexpr int kAtThreads = kAtWarps * 32;
+constexpr int kStageTok = 32;                       // tokens per warp stage: two cache tiles
+constexpr int kStepTok = kAtWarps * kStageTok;      // tokens per CTA step
+constexpr int kAtStages = 3;
+constexpr float kPShift = 15.0f;                    // P carries 2^15
+constexpr int kAtMaxCtasPerSm = 4;
+
+struct AtArgs {
+  const uint16_t* q;
+  const uint8_t* cache;
+  const int* table;
+  const int* lens;
+  const int* cu_q;
+  uint16_t* out;
+  float* lse;
+  float* slots;         // [2 * ctas][RT * (D + 2)]
+  unsigned* counters;   // [batch][heads][tiles_max]
+  long long q_stride, out_stride;
+  int batch, total_q, max_q, heads, q_heads, per, page_log2, pages, max_pages, tiles_max;
+  float scale_log2;     // scale * log2(e)
+  int window, split, bf16;
+};
+
+// Host and device agree on the rows per tile.
+template <int D, int NT>
+struct AtCfg {
+  static constexpr int RT = 8 * NT;
+  static constexpr int PART = RT * (D + 2);   // fp32 per partial: O, m, l
+};
+
+__device__ __forceinline__ void at_cp16(uint32_t saddr, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(saddr), "l"(src) : "memory");
+}
+__device__ __forceinline__ void at_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void at_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t at_hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Nibbles (0, 4), (1, 5), (2, 6), (3, 7) of w minus the integer behind the
+// biases: bias = 1024 + z, bias16 = -(64 + z), both exact in fp16.
+__device__ __forceinline__ void decode_nibbles(uint32_t w, uint32_t bias, uint32_t bias16, uint32_t (&a)[4]) {
+  const uint32_t w8 = w >> 8;
+  a[0] = hsub2_u(lop3_and_or(w, 0x000F000Fu, 0x64006400u), bias);
+  a[1] = hfma2_u(lop3_and_or(w, 0x00F000F0u, 0x64006400u), 0x2C002C00u, bias16);
+  a[2] = hsub2_u(lop3_and_or(w8, 0x000F000Fu, 0x64006400u), bias);
+  a[3] = hfma2_u(lop3_and_or(w8, 0x00F000F0u, 0x64006400u), 0x2C002C00u, bias16);
+}
+// The biases of a pair of zero-points (fp16, integers 0 .. 15): 1024 + z and
+// -64 - z by exact fp16 additions.
+__device__ __forceinline__ void zero_biases(uint32_t z, uint32_t& bias, uint32_t& bias16) {
+  bias = hfma2_u(z, 0x3C003C00u, 0x64006400u);
+  bias16 = hfma2_u(z, 0xBC00BC00u, 0xD400D400u);
+}
+
+// What a sequence asks for.
+struct Seq {
+  int len, q0, nq, rows, tiles, steps;
+  int first, lo;   // first token any of its queries sees; the same down to a stage border
+};
+
+__device__ __forceinline__ Seq seq_of(const AtArgs& a, int b, int RT) {
+  Seq s;
+  const long long most = (long long)a.max_pages << a.page_log2;
+  const int len = a.lens[b];
+  s.len = len < 0 ? 0 : (len > most ? (int)most : len);
+  if (a.cu_q) {
+    const int e0 = a.cu_q[b], e1 = a.cu_q[b + 1];
+    s.q0 = min(max(e0, 0), a.total_q);
+    s.nq = min(min(max(e1, s.q0), a.total_q) - s.q0, a.max_q);
+  } else {
+    s.q0 = b;
+    s.nq = b < a.total_q ? 1 : 0;
+  }
+  s.rows = s.nq * a.per;
+  s.tiles = (s.rows + RT - 1) / RT;
+  s.first = a.window > 0 ? max(0, s.len - s.nq - a.window + 1) : 0;
+  s.lo = s.first & ~(kStageTok - 1);
+  s.steps = max(1, (s.len - s.lo + kStepTok - 1) / kStepTok);
+  return s;
+}
+
+template <int D, int MODE, int GD, int NT>
+__global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMaxCtasPerSm)
+    kv_attend_kernel(const AtArgs a) {
+  constexpr int RT = AtCfg<D, NT>::RT;
+  constexpr int G = D / GD;
+  constexpr int PB = kv_param_bytes(MODE);
+  constexpr int TB = kv_tile_bytes(D, G, MODE);
+  constexpr int KROW = D / 2;                 // bytes of a code row
+  constexpr int V_OFF = 16 * KROW, KP_OFF = 32 * KROW, VP_OFF = KP_OFF + 16 * G * PB;
+  constexpr int KW = D / 32;                  // key words per lane and token: one per 32 dims
+  constexpr int VW = D / 64;                  // value words per lane and token
+  constexpr int MT = D / 16;                  // value MMA tiles
+  constexpr int STAGE = 2 * TB;
+  // token at place k of the MMA's k order (and S's rows): see kv.cuh, the
+  // rows read together must sit in different banks
+  constexpr int SX = D == 64 ? 2 : 1;
+
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ long long s_scan[kAtWarps];
+  __shared__ long long s_base[2];
+  __shared__ int s_b0;
+  __shared__ int s_last;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  unsigned char* ring = smem + warp * (kAtStages * STAGE);
+  const uint32_t ring_s = smem_u32(ring);
+
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- steps of all sequences, and this CTA's range of them
+  auto units_of = [&](int b) -> long long {
+    const Seq s = seq_of(a, b, RT);
+    return (long long)s.tiles * a.heads * s.steps;
+  };
+  long long total = 0;
+  for (int b = threadIdx.x; b < a.batch; b += kAtThreads) total += units_of(b);
+#pragma unroll
+  for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
+  if (lane == 0) s_scan[warp] = total;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kAtWarps; ++w) total += s_scan[w];
+  if (total == 0) return;
+  const long long U = total;
+  const long long C = U < (long long)gridDim.x ? U : (long long)gridDim.x;   // CTAs with work
+  const long long c = blockIdx.x;
+  if (c >= C) return;
+  long long u = c * U / C, u_end = (c + 1) * U / C;
+
+  // the sequence that holds unit u, and its first unit
+  {
+    long long base = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kAtThreads) {
+      const int b = b0 + threadIdx.x;
+      const long long n = b < a.batch ? units_of(b) : 0;
+      long long inc = n;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, inc, m);
+        if (lane >= m) inc += o;
+      }
+      __syncthreads();
+      if (lane == 31) s_scan[warp] = inc;
+      __syncthreads();
+      long long before = base, all = base;
+#pragma unroll
+      for (int w = 0; w < kAtWarps; ++w) {
+        if (w < warp) before += s_scan[w];
+        all += s_scan[w];
+      }
+      const long long lo = before + inc - n;
+      if (n > 0 && lo <= u && u < lo + n) {
+        s_b0 = b;
+        s_base[0] = lo;
+      }
+      base = all;
+      if (base > u) break;   // the same for every thread
+    }
+    __syncthreads();
+  }
+  int b = s_b0;
+  long long b_first = s_base[0];
+  Seq sq = seq_of(a, b, RT);
+
+  if (!a.split) {
+    // whole tiles only: those that start inside the range
+    auto up = [&](long long v) {
+      // first tile start at or after v (v in or after sequence b)
+      int bb = b;
+      long long f = b_first;
+      Seq s = sq;
+      while (true) {
+        const long long n = (long long)s.tiles * a.heads * s.steps;
+        if (v < f + n || bb + 1 >= a.batch) break;
+        f += n;
+        s = seq_of(a, ++bb, RT);
+      }
+      const long long r = (v - f) % s.steps;
+      return r == 0 ? v : v + s.steps - r;
+    };
+    const long long ub = up(u), ue = u_end >= U ? U : up(u_end);
+    u = ub;
+    u_end = ue;
+  }
+  bool first_seg = true;
+
+  while (u < u_end) {
+    while (u >= b_first + (long long)sq.tiles * a.heads * sq.steps) {   // next sequence with work
+      b_first += (long long)sq.tiles * a.heads * sq.steps;
+      sq = seq_of(a, ++b, RT);
+    }
+    const int tile_in = (int)((u - b_first) / sq.steps);
+    const int s0 = (int)(u - b_first - (long long)tile_in * sq.steps);
+    const int s1 = (int)min((long long)sq.steps, s0 + (u_end - u));
+    const int head = tile_in % a.heads, rt = tile_in / a.heads;
+
+    // ---- this lane's query rows: column g of each token tile as operand,
+    // columns 2t, 2t + 1 of the sums
+    uint32_t qf[NT][2 * KW][2];
+    float qs[NT][2];       // scale log2(e) / (power of two of the row)
+    int hi_q[NT][2], lo_q[NT][2];
+    int full_hi = sq.len, full_lo = 0;   // tokens every row of the tile sees
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = rt * RT + nt * 8 + g;
+      const bool ok = row < sq.rows;
+      const int qi = ok ? row / a.per : 0, hq = ok ? row - qi * a.per : 0;
+      const uint16_t* src = a.q + (long long)(sq.q0 + qi) * a.q_stride + (head * a.per + hq) * D;
+      float inv = a.scale_log2;
+      uint4 v[KW];
+#pragma unroll
+      for (int w = 0; w < KW; ++w)
+        v[w] = ok ? *reinterpret_cast<const uint4*>(src + 32 * w + 8 * t) : make_uint4(0, 0, 0, 0);
+      float mul = 1.0f;
+      if (a.bf16) {
+        uint32_t top = 0;   // largest magnitude bits of the row
+#pragma unroll
+        for (int w = 0; w < KW; ++w)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t x = (&v[w].x)[k];
+            top = max(top, max(x & 0x7FFFu, (x >> 16) & 0x7FFFu));
+          }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^(14 - e) for the largest's exponent e, held inside fp32's normals
+        const int e = (int)(top >> 7) - 127;
+        const int k = min(max(14 - e, -126), 126);
+        mul = __int_as_float((127 + k) << 23);
+        inv *= __int_as_float((127 - k) << 23);
+      }
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        uint32_t x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[k] = (&v[w].x)[k];
+          if (a.bf16)
+            x[k] = pack2<false>(__uint_as_float(x[k] << 16) * mul, __uint_as_float(x[k] & 0xFFFF0000u) * mul);
+        }
+        // dims (p, p + 4) of the word: the pairs the decoder yields
+        qf[nt][2 * w][0] = __byte_perm(x[0], x[2], 0x5410);
+        qf[nt][2 * w][1] = __byte_perm(x[0], x[2], 0x7632);
+        qf[nt][2 * w + 1][0] = __byte_perm(x[1], x[3], 0x5410);
+        qf[nt][2 * w + 1][1] = __byte_perm(x[1], x[3], 0x7632);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int col = 2 * t + i;
+        qs[nt][i] = __shfl_sync(0xffffffffu, inv, 4 * col);
+        const int r2 = rt * RT + nt * 8 + col;
+        if (r2 < sq.rows) {
+          const int pos = sq.len - sq.nq + r2 / a.per;
+          hi_q[nt][i] = pos + 1;
+          lo_q[nt][i] = a.window > 0 ? pos - a.window + 1 : 0;
+        } else {
+          hi_q[nt][i] = lo_q[nt][i] = 0;
+        }
+      }
+    }
+    {
+      const int r0 = rt * RT, r1 = min(sq.rows, r0 + RT) - 1;
+      full_hi = sq.len - sq.nq + r0 / a.per + 1;
+      full_lo = a.window > 0 ? sq.len - sq.nq + r1 / a.per - a.window + 1 : 0;
+    }
+
+    float oacc[MT][NT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) oacc[i][nt][k] = 0.0f;
+    float mrow[NT][2], lrow[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mrow[nt][i] = -INFINITY;
+        lrow[nt][i] = 0.0f;
+      }
+
+    // ---- copies of this warp's 32 tokens of step s into ring stage st
+    const int* trow = a.table + (long long)b * a.max_pages;
+    auto token0 = [&](int s) { return sq.lo + (s * kAtWarps + warp) * kStageTok; };
+    auto issue = [&](int s, int st) {
+      const int t0 = token0(s);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int tt = t0 + 16 * j;
+        if (tt < sq.len) {   // warp-uniform
+          int id = trow[tt >> a.page_log2];
+          if ((unsigned)id >= (unsigned)a.pages) id = 0;   // no access outside the cache
+          const long long tile = ((long long)id * a.heads + head) * (1 << (a.page_log2 - 4)) +
+                                 ((tt & ((1 << a.page_log2) - 1)) >> 4);
+          const uint8_t* src = a.cache + tile * TB + lane * 16;
+          const uint32_t dst = ring_s + st * STAGE + j * TB + lane * 16;
+#pragma unroll
+          for (int i = 0; i < TB / 512; ++i) at_cp16(dst + i * 512, src + i * 512);
+          if (TB % 512 != 0 && lane * 16 < TB % 512) at_cp16(dst + TB / 512 * 512, src + TB / 512 * 512);
+        }
+      }
+    };
+
+#pragma unroll
+    for (int s = 0; s < kAtStages - 1; ++s) {
+      if (s0 + s < s1) issue(s0 + s, s);
+      at_commit();
+    }
+    int st_c = 0, st_f = kAtStages - 1;
+    for (int s = s0; s < s1; ++s) {
+      if (s + kAtStages - 1 < s1) issue(s + kAtStages - 1, st_f);
+      at_commit();
+      at_wait<kAtStages - 1>();
+      __syncwarp();
+      const int t0 = token0(s);
+      if (t0 < sq.len) {   // warp-uniform
+        const unsigned char* stage = ring + st_c * STAGE;
+        const bool full = t0 + kStageTok <= full_hi && t0 >= full_lo;
+        const int tau0 = (g & 1) ? 4 + ((g >> 1) ^ SX) : (g >> 1);   // token of S's row g
+
+        // ---- S^T = K~ Q^T for the two 16-token tiles
+        float x[2][NT][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const unsigned char* tp = stage + j * TB;
+          uint32_t kw[2][KW];   // rows g, g + 8
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const unsigned char* rp = tp + (tau0 + 8 * h) * KROW;
+            if constexpr (D == 64) {
+              const uint2 v = *reinterpret_cast<const uint2*>(rp + 8 * t);
+              kw[h][0] = v.x;
+              kw[h][1] = v.y;
+            } else {
+#pragma unroll
+              for (int i = 0; i < KW / 4; ++i) {
+                const int piece = (t + 4 * i) ^ (D == 256 ? 4 * (tau0 & 1) : 0);
+                const uint4 v = *reinterpret_cast<const uint4*>(rp + 16 * piece);
+                kw[h][4 * i] = v.x;
+                kw[h][4 * i + 1] = v.y;
+                kw[h][4 * i + 2] = v.z;
+                kw[h][4 * i + 3] = v.w;
+              }
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[j][nt][i] = 0.0f;
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr) {
+            float sc[2];
+            uint32_t bias[2] = {0x64086408u, 0x64086408u}, bias16[2] = {0xD480D480u, 0xD480D480u};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const unsigned char* pp = tp + KP_OFF + ((tau0 + 8 * h) * G + gr) * PB;
+              if constexpr (MODE == kASYM) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(pp);
+                sc[h] = __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu)));
+                zero_biases(__byte_perm(w, 0, 0x3232), bias[h], bias16[h]);
+              } else {
+                sc[h] = __half2float(*reinterpret_cast<const __half*>(pp));
+              }
+            }
+            float part[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) part[nt][i] = 0.0f;
+#pragma unroll
+            for (int w = gr * (GD / 32); w < (gr + 1) * (GD / 32); ++w) {
+              uint32_t d0[4], d1[4];
+              decode_nibbles(kw[0][w], bias[0], bias16[0], d0);
+              decode_nibbles(kw[1][w], bias[1], bias16[1], d1);
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const uint32_t af[4] = {d0[2 * half], d1[2 * half], d0[2 * half + 1], d1[2 * half + 1]};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_16816<false>(part[nt], af, qf[nt][2 * w + half][0], qf[nt][2 * w + half][1]);
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[j][nt][i] = fmaf(sc[i >> 1], part[nt][i], x[j][nt][i]);
+          }
+        }
+
+        // ---- running softmax
+        uint32_t pf[2][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float alpha[2], mnew[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float mx = mrow[nt][i];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float v = x[j][nt][2 * h + i] * qs[nt][i];
+                if (!full) {
+                  const int tok = t0 + 16 * j + 8 * h + tau0;
+                  if (tok >= hi_q[nt][i] || tok < lo_q[nt][i]) v = -INFINITY;
+                }
+                x[j][nt][2 * h + i] = v;
+                mx = fmaxf(mx, v);
+              }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            mnew[i] = mx;
+            const float ref = mx == -INFINITY ? 0.0f : mx;   // nothing seen yet
+            alpha[i] = exp2_fast(mrow[nt][i] - ref);
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float p = exp2_fast(x[j][nt][2 * h + i] - ref + kPShift);
+                x[j][nt][2 * h + i] = p;
+                sum += p;
+              }
+            lrow[nt][i] = lrow[nt][i] * alpha[i] + sum;
+          }
+          if (__any_sync(0xffffffffu, mnew[0] != mrow[nt][0] || mnew[1] != mrow[nt][1])) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) oacc[mt][nt][k] *= alpha[k & 1];
+            mrow[nt][0] = mnew[0];
+            mrow[nt][1] = mnew[1];
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              pf[j][nt][h] = transpose8x8(pack2<false>(x[j][nt][2 * h], x[j][nt][2 * h + 1]));
+        }
+
+        // ---- O^T += V~^T P^T
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const unsigned char* tp = stage + j * TB;
+          int tok[4];
+          tok[0] = t;
+          tok[1] = 4 + (t ^ SX);
+          tok[2] = 8 + t;
+          tok[3] = 12 + (t ^ SX);
+          uint32_t vw[4][VW];
+          uint32_t par[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const unsigned char* rp = tp + V_OFF + tok[k] * KROW + (D / 16) * kv_val_piece(D, g, tok[k]);
+            if constexpr (D == 64) {
+              vw[k][0] = *reinterpret_cast<const uint32_t*>(rp);
+            } else if constexpr (D == 128) {
+              const uint2 v = *reinterpret_cast<const uint2*>(rp);
+              vw[k][0] = v.x;
+              vw[k][1] = v.y;
+            } else {
+              const uint4 v = *reinterpret_cast<const uint4*>(rp);
+              vw[k][0] = v.x;
+              vw[k][1] = v.y;
+              vw[k][2] = v.z;
+              vw[k][3] = v.w;
+            }
+            const unsigned char* pp = tp + VP_OFF + (tok[k] * G + g * (D / 8) / GD) * PB;
+            if constexpr (MODE == kASYM) par[k] = *reinterpret_cast<const uint32_t*>(pp);
+            else par[k] = *reinterpret_cast<const uint16_t*>(pp);
+            // what lies past the sequence or before its window may be anything,
+            // and 0 times a NaN found there is a NaN: its scale reads as 0
+            const int pos = t0 + 16 * j + tok[k];
+            if (!full && (pos >= sq.len || pos < sq.first)) par[k] = 0;
+          }
+          uint32_t sv[2], bias[2] = {0x64086408u, 0x64086408u}, bias16[2] = {0xD480D480u, 0xD480D480u};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            sv[h] = __byte_perm(par[2 * h], par[2 * h + 1], 0x5410);
+            if constexpr (MODE == kASYM)
+              zero_biases(__byte_perm(par[2 * h], par[2 * h + 1], 0x7632), bias[h], bias16[h]);
+          }
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {   // dims 4 half .. 4 half + 3 of the word
+              uint32_t d[2][4];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t u2 = __byte_perm(vw[2 * h][w], vw[2 * h + 1][w], half ? 0x7632 : 0x5410);
+                decode_nibbles(u2, bias[h], bias16[h], d[h]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) d[h][k] = at_hmul2(d[h][k], sv[h]);
+              }
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t af[4] = {d[0][2 * e], d[0][2 * e + 1], d[1][2 * e], d[1][2 * e + 1]};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_16816<false>(oacc[4 * w + 2 * half + e][nt], af, pf[j][nt][0], pf[j][nt][1]);
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();   // every lane is done with the stage before it is refilled
+      st_c = st_c + 1 == kAtStages ? 0 : st_c + 1;
+      st_f = st_f + 1 == kAtStages ? 0 : st_f + 1;
+    }
+    at_wait<0>();
+
+    // ---- the warps' results through shared memory (the rings are idle)
+    __syncthreads();
+    float* wm = reinterpret_cast<float*>(smem);             // [warps][RT]
+    float* wl = wm + kAtWarps * RT;                         // [warps][RT]
+    float* wo = wl + kAtWarps * RT;                         // [warps][RT][D]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float l = lrow[nt][i];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int row = nt * 8 + 2 * t + i;
+        if (g == 0) {
+          wm[warp * RT + row] = mrow[nt][i];
+          wl[warp * RT + row] = l;
+        }
+        float* dst = wo + (warp * RT + row) * D + g * (D / 8);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          *reinterpret_cast<float2*>(dst + 2 * mt) = make_float2(oacc[mt][nt][i], oacc[mt][nt][2 + i]);
+      }
+    __syncthreads();
+
+    const bool whole = s0 == 0 && s1 == sq.steps;
+    const int rows_here = min(RT, sq.rows - rt * RT);
+    auto emit = [&](int row, int d4, const float4& o, float m, float l) {
+      // four dims of a row: o / l (0 for a row that sees nothing)
+      const int r2 = rt * RT + row, qi = r2 / a.per, hq = head * a.per + r2 - qi * a.per;
+      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+      uint2 v;
+      if (a.bf16) {
+        v.x = pack2<true>(o.x * inv, o.y * inv);
+        v.y = pack2<true>(o.z * inv, o.w * inv);
+      } else {
+        v.x = pack2<false>(o.x * inv, o.y * inv);
+        v.y = pack2<false>(o.z * inv, o.w * inv);
+      }
+      *reinterpret_cast<uint2*>(a.out + (long long)(sq.q0 + qi) * a.out_stride + hq * D + d4) = v;
+      if (d4 == 0 && a.lse)
+        a.lse[(long long)(sq.q0 + qi) * a.q_heads + hq] =
+            l == 0.0f ? -INFINITY : 0.69314718056f * (m + log2f(l) - kPShift);
+    };
+    float* slot = a.slots + (2 * c + (first_seg ? 0 : 1)) * (long long)AtCfg<D, NT>::PART;
+    for (int i = threadIdx.x; i < rows_here * (D / 4); i += kAtThreads) {
+      const int row = i / (D / 4), d4 = (i % (D / 4)) * 4;
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kAtWarps; ++w) m = fmaxf(m, wm[w * RT + row]);
+      const float ref = m == -INFINITY ? 0.0f : m;
+      float l = 0.0f;
+      float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int w = 0; w < kAtWarps; ++w) {
+        const float f = exp2_fast(wm[w * RT + row] - ref);
+        const float4 v = *reinterpret_cast<const float4*>(wo + (w * RT + row) * D + d4);
+        l = fmaf(f, wl[w * RT + row], l);
+        o.x = fmaf(f, v.x, o.x);
+        o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z);
+        o.w = fmaf(f, v.w, o.w);
+      }
+      if (whole) {
+        emit(row, d4, o, m, l);
+      } else {
+        *reinterpret_cast<float4*>(slot + row * D + d4) = o;
+        if (d4 == 0) {
+          slot[RT * D + row] = m;
+          slot[RT * D + RT + row] = l;
+        }
+      }
+    }
+    if (!whole) {
+      __syncthreads();
+      const long long t_first = b_first + (long long)tile_in * sq.steps;
+      const long long first = ((t_first + 1) * C - 1) / U;
+      const long long nb = ((t_first + sq.steps) * C - 1) / U - first + 1;
+      unsigned* counter = a.counters + ((long long)b * a.heads + head) * a.tiles_max + rt;
+      if (threadIdx.x == 0) {
+        unsigned prev;
+        asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;" : "=r"(prev) : "l"(counter) : "memory");
+        s_last = prev == (unsigned)(nb - 1);
+      }
+      __syncthreads();
+      if (s_last) {
+        // `first` left its partial in its second slot if its range began before the tile
+        const int first_e = first * U / C < t_first ? 1 : 0;
+        for (int i = threadIdx.x; i < rows_here * (D / 4); i += kAtThreads) {
+          const int row = i / (D / 4), d4 = (i % (D / 4)) * 4;
+          float m = -INFINITY, l = 0.0f;
+          float4 o = make_float4(0, 0, 0, 0);
+          for (long long k = 0; k < nb; ++k) {
+            const float* p = a.slots + (2 * (first + k) + (k == 0 ? first_e : 0)) * (long long)AtCfg<D, NT>::PART;
+            const float mk = __ldcg(p + RT * D + row), lk = __ldcg(p + RT * D + RT + row);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p + row * D + d4));
+            const float mn = fmaxf(m, mk);
+            const float ref = mn == -INFINITY ? 0.0f : mn;
+            const float fa = exp2_fast(m - ref), fb = exp2_fast(mk - ref);
+            m = mn;
+            l = l * fa + lk * fb;
+            o.x = o.x * fa + v.x * fb;
+            o.y = o.y * fa + v.y * fb;
+            o.z = o.z * fa + v.z * fb;
+            o.w = o.w * fa + v.w * fb;
+          }
+          emit(row, d4, o, m, l);
+        }
+        if (threadIdx.x == 0) *counter = 0u;   // ready for the next call
+      }
+    }
+    __syncthreads();   // shared memory is reused by the next tile
+    first_seg = false;
+    u += s1 - s0;
+  }
+}
+
+template <int D, int MODE, int GD, int NT>
+cudaError_t at_launch(const AtArgs& args, long long most, cudaStream_t stream) {
+  auto k = kv_attend_kernel<D, MODE, GD, NT>;
+  constexpr int RT = AtCfg<D, NT>::RT;
+  constexpr size_t ring = (size_t)kAtWarps * kAtStages * 2 * kv_tile_bytes(D, D / GD, MODE);
+  constexpr size_t red = (size_t)kAtWarps * RT * (D + 2) * sizeof(float);
+  constexpr size_t smem = ring > red ? ring : red;
+  static_assert(smem <= 227 * 1024, "shared memory of the attention kernel");
+  static int occ[64] = {};   // resident CTAs per SM, once per device
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!occ[dev]) {
+    int o = 0;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, k, kAtThreads, smem);
+    if (e == cudaSuccess && o < 1) e = cudaErrorInvalidConfiguration;
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return e;
+    }
+    occ[dev] = o;
+  }
+  const int ctas = (int)std::min<long long>(
+      std::min((long long)occ[dev], (long long)kAtMaxCtasPerSm) * device_sms(), most);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(kAtThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, args);
+  if (e != cudaSuccess) cudaGetLastError();   // report it once, here
+  return e;
+}
+
+// Query rows per tile: 8 for a key head with up to 8 rows (and for 256 dims,
+// whose sums need the registers), else 16.
+int at_rows(int max_q, int per, int dim) {
+  return (long long)max_q * per <= 8 || dim == 256 ? 8 : 16;
+}
+
+struct AtPlan {
+  int rows, tiles_max, ctas;
+  size_t counters, slots;
+};
+
+AtPlan at_plan(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms) {
+  AtPlan p{};
+  const int per = q_heads / kv_heads;
+  p.rows = at_rows(max_q, per, dim);
+  p.tiles_max = (int)(((long long)max_q * per + p.rows - 1) / p.rows);
+  p.ctas = sms * kAtMaxCtasPerSm;
+  p.counters = ((size_t)batch * kv_heads * p.tiles_max * sizeof(unsigned) + 255) / 256 * 256;
+  p.slots = (size_t)2 * p.ctas * p.rows * (dim + 2) * sizeof(float);
+  return p;
+}
+
+}  // namespace
+
+size_t kv_attend_workspace(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms) {
+  const AtPlan p = at_plan(batch, max_q, q_heads, kv_heads, dim, sms);
+  return p.counters + p.slots;
+}
+
+cudaError_t launch_kv_attend(const KvAttend& p, void* workspace, cudaStream_t stream) {
+  const KvCache& c = p.cache;
+  const AtPlan plan = at_plan(p.batch, p.max_q, p.q_heads, c.heads, c.dim, device_sms());
+  AtArgs a{};
+  a.q = static_cast<const uint16_t*>(p.q);
+  a.cache = static_cast<const uint8_t*>(c.data);
+  a.table = p.table;
+  a.lens = p.lens;
+  a.cu_q = p.cu_q;
+  a.out = static_cast<uint16_t*>(p.out);
+  a.lse = p.lse;
+  a.q_stride = p.q_stride;
+  a.out_stride = p.out_stride;
+  a.batch = p.batch;
+  a.total_q = p.total_q;
+  a.max_q = p.max_q;
+  a.heads = c.heads;
+  a.q_heads = p.q_heads;
+  a.per = p.q_heads / c.heads;
+  a.page_log2 = c.page_log2;
+  a.pages = c.pages;
+  a.max_pages = p.max_pages;
+  a.tiles_max = plan.tiles_max;
+  a.scale_log2 = p.scale * 1.4426950408889634f;
+  a.window = p.window;
+  a.bf16 = p.bf16;
+  if (workspace) {
+    a.split = 1;
+    a.counters = static_cast<unsigned*>(workspace);
+    a.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.counters);
+  }
+  // no more CTAs than steps the table could hold
+  const long long steps = std::max<long long>(1, (((long long)p.max_pages << c.page_log2) + kStepTok - 1) / kStepTok);
+  const long long most = (long long)p.batch * c.heads * plan.tiles_max * steps;
+  const int gd = c.dim / c.G;
+#define AT_CASE(D, MO, GD, NT) \
+  if (c.dim == D && c.mode == MO && gd == GD && plan.rows == 8 * NT) return at_launch<D, MO, GD, NT>(a, most, stream);
+#define AT_MODES(D, GD, NT) AT_CASE(D, kSYM, GD, NT) AT_CASE(D, kASYM, GD, NT)
+  AT_MODES(64, 32, 1) AT_MODES(64, 64, 1) AT_MODES(64, 32, 2) AT_MODES(64, 64, 2)
+  AT_MODES(128, 32, 1) AT_MODES(128, 64, 1) AT_MODES(128, 128, 1)
+  AT_MODES(128, 32, 2) AT_MODES(128, 64, 2) AT_MODES(128, 128, 2)
+  AT_MODES(256, 32, 1) AT_MODES(256, 64, 1) AT_MODES(256, 128, 1) AT_MODES(256, 256, 1)
+#undef AT_MODES
+#undef AT_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace qk

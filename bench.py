@@ -89,7 +89,8 @@ ZOPTS = {"asym_rowscale_zg8_u4": (8, 4), "llama70b_asym_zq4_bf16": (128, 4)}
 ACTORDER = {"actorder_llama7b"}
 SIGMA = {"sym": 0.02, "asym": 0.015, "lut": 0.02}
 L2_BYTES = 126 * 1000 * 1000     # B200 L2
-SKINNY_SOURCES = ("weight_only_quantized_int4_b200/csrc/skinny.cu",
+SKINNY_SOURCES = ("weight_only_quantized_int4_b200/csrc/skinny.cuh",
+                  "weight_only_quantized_int4_b200/csrc/skinny.cu",
                   "weight_only_quantized_int4_b200/csrc/common.cuh")
 
 

@@ -226,6 +226,29 @@ int qmm_gated(const void* x, int xdtype, const void* qweight, const uint16_t* sc
               const uint16_t* zeros_or_lut, int M, int I, int K, int bits, int group, int mode,
               void* y, void* workspace, size_t workspace_bytes, void* stream);
 
+/* The product with what a layer does to it next (an addition of this library):
+ *
+ *     y[M, N] = residual + act(x . dequant(Wq)^T + bias)
+ *
+ *   bias      device, [N], dtype of x, or NULL.
+ *   act       QMM_ACT_*: none, max(v, 0), v Phi(v) (GELU, by erfc), its tanh form
+ *             v / (1 + exp(-2 sqrt(2/pi) (v + 0.044715 v^3))), v / (1 + exp(-v)).
+ *   residual  device, [M, N], dtype of x, or NULL; it may be y itself (added onto in
+ *             place) but not overlap it otherwise; bias must not overlap y.
+ * Everything is taken in fp32 on the fp32 sums and rounded once.  The other
+ * arguments, the formats, paths, workspace and statuses are those of qmm. */
+typedef enum {
+  QMM_ACT_NONE = 0,
+  QMM_ACT_RELU = 1,
+  QMM_ACT_GELU = 2,
+  QMM_ACT_GELU_TANH = 3,
+  QMM_ACT_SILU = 4
+} qmm_act;
+int qmm_epilogue(const void* x, int xdtype, const void* qweight, const uint16_t* scales,
+                 const uint16_t* zeros_or_lut, const void* bias, int act, const void* residual, int M, int N,
+                 int K, int bits, int group, int mode, void* y, void* workspace, size_t workspace_bytes,
+                 void* stream);
+
 /* ---- Zero-point options (asymmetric 4-bit codes).
  *
  * "Does Marlin support zero-point quantization?" (IST-DASLab/marlin issue 5):

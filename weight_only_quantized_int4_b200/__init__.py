@@ -24,6 +24,7 @@ LIB_PATH = os.path.join(_HERE, "libqmm.so")
 MODES = {"sym": 0, "asym": 1, "lut": 2}
 DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 PATHS = {"auto": 0, "skinny": 1, "tensor": 2, "skinny_streamk": 3}
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 PATH_NAMES = {1: "skinny", 2: "tensor"}
 
 SYMBOLS = ("qmm_packed_size", "qmm_pack", "qmm_workspace_size", "qmm_workspace_size_for", "qmm",
@@ -32,7 +33,7 @@ SYMBOLS = ("qmm_packed_size", "qmm_pack", "qmm_workspace_size", "qmm_workspace_s
            "qmm_pack_gated", "qmm_gated", "qmm_zeros_size", "qmm_pack_asym",
            "qmm_workspace_size_asym", "qmm_asym", "qmm_dequant_asym", "qmm_actorder_perm",
            "qmm_pack_actorder", "qmm_workspace_size_actorder", "qmm_actorder",
-           "qmm_set_wait_limit", "qmm_kv_cache_size", "qmm_kv_store", "qmm_kv_load",
+           "qmm_set_wait_limit", "qmm_epilogue", "qmm_kv_cache_size", "qmm_kv_store", "qmm_kv_load",
            "qmm_kv_workspace_size", "qmm_kv_attend")
 
 _lib = None
@@ -82,6 +83,7 @@ def load(path: str = LIB_PATH):
             lib.qmm_workspace_size_actorder.argtypes = [I, I, I, I, I, I]
             lib.qmm_workspace_size_actorder.restype = S
             lib.qmm_actorder.argtypes = [P, I, P, P, P, P, I, I, I, I, I, I, P, P, S, P]
+            lib.qmm_epilogue.argtypes = [P, I, P, P, P, P, I, P, I, I, I, I, I, I, P, P, S, P]
             L, F = ctypes.c_longlong, ctypes.c_float
             lib.qmm_kv_cache_size.argtypes = [I, I, I, I, I, I]
             lib.qmm_kv_cache_size.restype = S
@@ -240,6 +242,33 @@ def qmm(x, qweight, scales, zeros_or_lut, N, K, mode, bits=4, group=128, y=None,
     _check(load().qmm_with_path(_ptr(x), DTYPES[x.dtype], _ptr(qweight), _ptr(scales),
                                 _ptr(zeros_or_lut), M, N, K, bits, group, MODES[mode], _ptr(y),
                                 _ptr(ws), nbytes, _stream(), PATHS[path]), "qmm")
+    return y
+
+
+def qmm_epilogue(x, qweight, scales, zeros_or_lut, N, K, mode, bits=4, group=128, bias=None, act="none",
+                 residual=None, y=None, ws=None):
+    """y[M, N] = residual + act(x[M, K] . dequant(qweight)^T + bias), rounded once.
+
+    bias [N] and residual [M, N] are of x's type, or None; act: a name of ACTS.
+    residual may be y itself (the product is added onto it in place).  ws as for qmm."""
+    _here("x", x, *DTYPES)
+    _dev(x, "x")
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError("x must be [M, K]")
+    M = x.shape[0]
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}")
+    if y is None:
+        y = torch.empty(M, N, dtype=x.dtype, device=x.device)
+    for name, t, shape in (("bias", bias, (N,)), ("residual", residual, (M, N)), ("y", y, (M, N))):
+        if t is not None:
+            _here(name, t, x.dtype)
+            if tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {list(shape)} tensor")
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(load().qmm_epilogue(_ptr(x), DTYPES[x.dtype], _ptr(qweight), _ptr(scales), _ptr(zeros_or_lut),
+                               _ptr(bias), ACTS[act], _ptr(residual), M, N, K, bits, group, MODES[mode],
+                               _ptr(y), _ptr(ws), nbytes, _stream()), "qmm_epilogue")
     return y
 
 

@@ -106,6 +106,18 @@ int choose_path(int M, int N, int bits, int mode, bool bf16, int group) {
   return QMM_PATH_TENSOR;
 }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+  return x < y + nb && y < x + na;
+}
+
+// What qmm_epilogue adds to a call of run_qmm.
+struct Epilogue {
+  const void* bias;
+  const void* residual;
+  int act;
+};
+
 // The plan a call runs with; `ws_bytes` is what it needs from the workspace.
 struct Plan {
   int path;
@@ -135,7 +147,8 @@ using namespace qk;
 static int run_qmm(const void* x, int xdtype, const void* qweight, const uint16_t* scales,
                    const uint16_t* zeros_or_lut, int M, int N, int K, int bits, int group,
                    int mode, void* y, void* workspace, size_t workspace_bytes, void* stream,
-                   int path, bool gated, int zgroup = 0, int zbits = 16) {
+                   int path, bool gated, int zgroup = 0, int zbits = 16,
+                   const Epilogue* epi = nullptr) {
   if (M < 0) return QMM_ERR_ARG;
   int st = check_shape(N, K, bits, group, zero_opts(mode) ? QMM_ASYM : mode);
   if (st != QMM_OK) return st;
@@ -158,6 +171,12 @@ static int run_qmm(const void* x, int xdtype, const void* qweight, const uint16_
   p.gated = gated;
   p.zgroup = zgroup;
   p.zbits = zbits;
+  if (epi) {
+    p.epilogue = true;
+    p.bias = epi->bias;
+    p.residual = epi->residual;
+    p.act = epi->act;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Plan plan = make_plan(M, N, K, bits, group, mode, xdtype == QMM_BF16, path);
   if (plan.ws_bytes()) {
@@ -266,6 +285,24 @@ int qmm_gated(const void* x, int xdtype, const void* qweight, const uint16_t* sc
   if (I % 16 != 0 || I > (1 << 19)) return QMM_ERR_UNSUPPORTED;
   return run_qmm(x, xdtype, qweight, scales, zeros_or_lut, M, 2 * I, K, bits, group, mode, y,
                  workspace, workspace_bytes, stream, QMM_PATH_AUTO, true);
+}
+
+int qmm_epilogue(const void* x, int xdtype, const void* qweight, const uint16_t* scales,
+                 const uint16_t* zeros_or_lut, const void* bias, int act, const void* residual, int M, int N,
+                 int K, int bits, int group, int mode, void* y, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+  if (act < QMM_ACT_NONE || act > QMM_ACT_SILU) return QMM_ERR_ARG;
+  if (!aligned(bias, 2) || !aligned(residual, 2)) return QMM_ERR_ALIGN;
+  if (mode != QMM_SYM && mode != QMM_ASYM && mode != QMM_LUT) return QMM_ERR_ARG;
+  if (M > 0 && N > 0 && y) {
+    const size_t ys = (size_t)M * N * 2;
+    if (bias && overlap(bias, (size_t)N * 2, y, ys)) return QMM_ERR_ARG;
+    // y itself is fine (each element is read by the thread that writes it)
+    if (residual && residual != y && overlap(residual, ys, y, ys)) return QMM_ERR_ARG;
+  }
+  const Epilogue e{bias, residual, act};
+  return run_qmm(x, xdtype, qweight, scales, zeros_or_lut, M, N, K, bits, group, mode, y, workspace,
+                 workspace_bytes, stream, QMM_PATH_AUTO, false, 0, 16, &e);
 }
 
 int qmm(const void* x, int xdtype, const void* qweight, const uint16_t* scales,

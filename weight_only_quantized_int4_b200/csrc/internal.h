@@ -21,6 +21,11 @@ struct Problem {
   // ASYM zero-point options (modes kASYMX / kASYMQ): zero group (columns; 0 =
   // the scale group, -1 = the row) and storage (16 = fp16, 4 = 4-bit integers)
   int zgroup = 0, zbits = 16;
+  // y = residual + act(sum + bias) (qmm_epilogue)
+  bool epilogue = false;
+  const void* bias = nullptr;
+  const void* residual = nullptr;
+  int act = 0;
 };
 
 // Split-K plan of the skinny (M <= 16 per slab) decode path.
@@ -41,6 +46,8 @@ SkinnyPlan plan_skinny(int M, int N, int K, int bits, int group, int mode, bool 
                        bool force_streamk = false);
 cudaError_t launch_skinny(const Problem& p, const SkinnyPlan& plan, void* workspace,
                           cudaStream_t stream);
+cudaError_t launch_skinny_epi(const Problem& p, const SkinnyPlan& plan, void* workspace,
+                              cudaStream_t stream);
 // Decode path on the library's static scratch buffer (no allocation); sets
 // *too_large instead of launching when the problem does not fit it.
 cudaError_t launch_skinny_static(const Problem& p, int sms, cudaStream_t stream, bool* too_large);
@@ -59,11 +66,14 @@ bool tc_supported(int bits, int mode, bool bf16, int group);
 TcPlan plan_tc(int M, int N, int K, int mode, bool bf16, int group, int sms);
 cudaError_t launch_tc(const Problem& p, const TcPlan& plan, void* workspace, long long wait_limit,
                       cudaStream_t stream);
+cudaError_t launch_tc_epi(const Problem& p, const TcPlan& plan, void* workspace, long long wait_limit,
+                          cudaStream_t stream);
 
 // Clock cycles a kernel's barrier wait may take before the call gives up
 // (qmm_set_wait_limit).
 long long wait_limit();
-unsigned tc_read_and_clear_error();
+unsigned tc_read_and_clear_error();       // of both files' kernels
+unsigned tc_epi_read_and_clear_error();
 
 // Quantize + pack.  W2: second matrix of the gated layout (else null); perm:
 // act-order column permutation (else null); zgroup / zbits: ASYM zero-point

@@ -51,7 +51,7 @@ def quantize(x, group, mode):
         if mode == "sym":
             z = np.full(s.shape, 8.0)
         else:
-            z = np.where(s > 0, np.clip(np.rint(-lo / d), 0, 15), 0.0)
+            z = np.where(s > 0, np.clip(np.rint(-lo / d), 0, 15), 0.0) + 0.0     # an integer: never -0
         q = np.clip(np.rint(g / d[..., None]) + z[..., None], 0, 15)
     q = np.where((s > 0)[..., None], q, z[..., None])
     return q.reshape(x.shape).astype(np.uint8), s, (z.astype(np.float16) if mode == "asym" else None)

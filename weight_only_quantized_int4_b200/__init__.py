@@ -124,6 +124,20 @@ def _stream():
     return torch.cuda.current_stream().cuda_stream
 
 
+# A call's checks are written out on plain attributes: a decode step makes these
+# calls once per layer, and the host must stay ahead of kernels of a few
+# microseconds.
+_cur_dev = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _bad_device(name):
+    return ValueError(f"{name} must be on the current CUDA device")
+
+
+def _stream_of(dev):
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
 def _check(status: int, what: str):
     if status != 0:
         raise QmmError(status, what)
@@ -245,30 +259,52 @@ def qmm(x, qweight, scales, zeros_or_lut, N, K, mode, bits=4, group=128, y=None,
     return y
 
 
+def _like_x(name, t, dev, dtype, shape):
+    if t.get_device() != dev:
+        raise _bad_device(name)
+    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}")
+
+
 def qmm_epilogue(x, qweight, scales, zeros_or_lut, N, K, mode, bits=4, group=128, bias=None, act="none",
                  residual=None, y=None, ws=None):
     """y[M, N] = residual + act(x[M, K] . dequant(qweight)^T + bias), rounded once.
 
     bias [N] and residual [M, N] are of x's type, or None; act: a name of ACTS.
     residual may be y itself (the product is added onto it in place).  ws as for qmm."""
-    _here("x", x, *DTYPES)
-    _dev(x, "x")
-    if x.dim() != 2 or x.shape[1] != K:
-        raise ValueError("x must be [M, K]")
+    dev, dtype = _cur_dev(), x.dtype
+    if x.get_device() != dev:
+        raise _bad_device("x")
+    if dtype not in DTYPES or x.dim() != 2 or x.shape[1] != K or not x.is_contiguous():
+        raise ValueError("x must be a contiguous fp16 or bf16 [M, K] tensor")
+    if qweight.get_device() != dev or scales.get_device() != dev:
+        raise _bad_device("qweight and scales")
+    if qweight.numel() * qweight.element_size() * 8 < N * K * bits:
+        raise ValueError("qweight is smaller than an [N, K] weight's codes")
     M = x.shape[0]
-    if act not in ACTS:
+    code = ACTS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {', '.join(ACTS)}")
+    bp = rp = wp = None
+    nbytes = 0
     if y is None:
-        y = torch.empty(M, N, dtype=x.dtype, device=x.device)
-    for name, t, shape in (("bias", bias, (N,)), ("residual", residual, (M, N)), ("y", y, (M, N))):
-        if t is not None:
-            _here(name, t, x.dtype)
-            if tuple(t.shape) != shape or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous {list(shape)} tensor")
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(load().qmm_epilogue(_ptr(x), DTYPES[x.dtype], _ptr(qweight), _ptr(scales), _ptr(zeros_or_lut),
-                               _ptr(bias), ACTS[act], _ptr(residual), M, N, K, bits, group, MODES[mode],
-                               _ptr(y), _ptr(ws), nbytes, _stream()), "qmm_epilogue")
+        y = torch.empty((M, N), dtype=dtype, device=x.device)
+    else:
+        _like_x("y", y, dev, dtype, (M, N))
+    if bias is not None:
+        _like_x("bias", bias, dev, dtype, (N,))
+        bp = bias.data_ptr()
+    if residual is not None:
+        if residual is not y:
+            _like_x("residual", residual, dev, dtype, (M, N))
+        rp = residual.data_ptr()
+    if ws is not None:
+        wp, nbytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    st = (_lib or load()).qmm_epilogue(x.data_ptr(), DTYPES[dtype], qweight.data_ptr(), scales.data_ptr(),
+                                       None if zeros_or_lut is None else zeros_or_lut.data_ptr(), bp, code, rp, M, N,
+                                       K, bits, group, MODES[mode], y.data_ptr(), wp, nbytes, _stream_of(dev))
+    if st:
+        raise QmmError(st, "qmm_epilogue")
     return y
 
 
@@ -404,44 +440,55 @@ def qmm_actorder(x, perm, qweight, scales, zeros_or_lut, N, K, mode, bits=4, gro
 
 # ---- 4-bit key / value cache and attention over it
 
-def _here(name, t, *dtypes):
-    """t is on the current device and of one of the dtypes (its kernel runs there)."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device")
-    if dtypes and t.dtype not in dtypes:
-        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}")
-
-
-def _token_rows(name, t, *dtypes):
-    """t is [tokens, heads, dim] with contiguous rows of heads: (heads, dim, token stride)."""
-    _here(name, t, *dtypes)
+def _token_rows(name, t, dev, dtype):
+    """(tokens, heads, dim, token stride) of a [tokens, heads, dim] tensor of `dtype`
+    on device `dev` whose tokens hold their heads contiguously."""
+    if t.get_device() != dev:
+        raise _bad_device(name)
+    if t.dtype is not dtype or dtype not in DTYPES:
+        raise ValueError(f"{name} must be fp16 or bf16, all of one type")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, dim]")
     T, H, D = t.shape
-    if T > 0 and ((D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D)):
+    st = t.stride()
+    if T == 0:
+        return T, H, D, H * D
+    if (st[2] != 1 and D > 1) or (st[1] != D and H > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    # a single token's stride says nothing
-    return H, D, t.stride(0) if T > 1 else H * D
+    return T, H, D, (st[0] if T > 1 else H * D)   # a single token's stride says nothing
 
 
-def _int_vector(name, t, n=None):
-    _here(name, t, torch.int32)
-    if t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must be a contiguous int32 vector" + ("" if n is None else f" of {n}"))
+def _int_vector(name, t, n, dev):
+    if t.get_device() != dev:
+        raise _bad_device(name)
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector of {n}")
 
 
-def _cache_shape(cache, dim, mode, group):
-    """(pages, heads, page) of a kv_cache() tensor of this format."""
-    _here("cache", cache, torch.uint8)
-    if cache.dim() != 4 or not cache.is_contiguous():
-        raise ValueError("cache must be a tensor of kv_cache()")
-    pages, heads, tiles, nbytes = cache.shape
-    want = load().qmm_kv_cache_size(pages, heads, dim, 16 * tiles, group, MODES[mode])
-    if want == 0:
-        raise QmmError(-2, "qmm_kv_cache_size")
-    if want != cache.numel():
-        raise ValueError(f"cache: tiles of {nbytes} bytes do not hold dim {dim}, {mode}, group {group}")
-    return pages, heads, 16 * tiles
+_cache_formats = {}   # (shape, dim, mode, group) -> (pages, heads, page, mode code)
+
+
+def _cache_shape(cache, dim, mode, group, dev):
+    """(pages, heads, page, mode code) of a kv_cache() tensor of this format."""
+    if cache.get_device() != dev:
+        raise _bad_device("cache")
+    shape = cache.shape
+    known = _cache_formats.get((shape, dim, mode, group))
+    if known is None:
+        if len(shape) != 4:
+            raise ValueError("cache must be a tensor of kv_cache()")
+        pages, heads, tiles, nbytes = shape
+        want = load().qmm_kv_cache_size(pages, heads, dim, 16 * tiles, group, MODES[mode])
+        if want == 0:
+            raise QmmError(-2, "qmm_kv_cache_size")
+        if want != pages * heads * tiles * nbytes:
+            raise ValueError(f"cache: tiles of {nbytes} bytes do not hold dim {dim}, {mode}, group {group}")
+        if len(_cache_formats) > 256:
+            _cache_formats.clear()
+        known = _cache_formats[(shape, dim, mode, group)] = (pages, heads, 16 * tiles, MODES[mode])
+    if cache.dtype is not torch.uint8 or not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous uint8 tensor")
+    return known
 
 
 def kv_cache(pages, heads, dim, page=64, mode="sym", group=-1, device="cuda"):
@@ -457,32 +504,41 @@ def kv_store(k, v, slots, cache, mode="sym", group=-1):
     """Quantize k[i], v[i] ([tokens, heads, dim], fp16 or bf16; slices of a fused
     projection are taken as they are) into slots[i] (int32: page index times the
     page length + place; negative: skipped) of the cache."""
-    H, D, ks = _token_rows("k", k, *DTYPES)
-    Hv, Dv, vs = _token_rows("v", v, k.dtype)
-    if (k.shape[0], H, D) != (v.shape[0], Hv, Dv):
+    dev, dtype = _cur_dev(), k.dtype
+    T, H, D, ks = _token_rows("k", k, dev, dtype)
+    Tv, Hv, Dv, vs = _token_rows("v", v, dev, dtype)
+    if T != Tv or H != Hv or D != Dv:
         raise ValueError("k and v must have the same shape")
-    _int_vector("slots", slots, k.shape[0])
-    pages, heads, page = _cache_shape(cache, D, mode, group)
+    _int_vector("slots", slots, T, dev)
+    pages, heads, page, code = _cache_shape(cache, D, mode, group, dev)
     if heads != H:
         raise ValueError(f"the cache holds {heads} heads, k has {H}")
-    _check(load().qmm_kv_store(_ptr(k), _ptr(v), DTYPES[k.dtype], ks, vs, _ptr(slots), k.shape[0], H, D,
-                               page, pages, group, MODES[mode], _ptr(cache), _stream()), "qmm_kv_store")
+    st = (_lib or load()).qmm_kv_store(k.data_ptr(), v.data_ptr(), DTYPES[dtype], ks, vs, slots.data_ptr(), T, H, D,
+                                       page, pages, group, code, cache.data_ptr(), _stream_of(dev))
+    if st:
+        raise QmmError(st, "qmm_kv_store")
 
 
 def kv_load(cache, slots, dim, mode="sym", group=-1, dtype=torch.float16, out=None):
     """The decoded keys and values ([tokens, heads, dim] each) of the given slots."""
-    _int_vector("slots", slots)
-    pages, heads, page = _cache_shape(cache, dim, mode, group)
-    shape = (slots.shape[0], heads, dim)
+    dev, T = _cur_dev(), slots.shape[0]
+    _int_vector("slots", slots, T, dev)
+    pages, heads, page, code = _cache_shape(cache, dim, mode, group, dev)
     if out is None:
-        out = tuple(torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
-    k, v = out
-    for name, t in (("k", k), ("v", v)):
-        _here(name, t, *DTYPES)
-        if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype != k.dtype:
-            raise ValueError(f"{name} must be a contiguous {list(shape)} tensor")
-    _check(load().qmm_kv_load(_ptr(cache), _ptr(slots), shape[0], heads, dim, page, pages, group, MODES[mode],
-                              DTYPES[k.dtype], _ptr(k), _ptr(v), _stream()), "qmm_kv_load")
+        if dtype not in DTYPES:
+            raise ValueError("dtype must be fp16 or bf16")
+        k = torch.empty((T, heads, dim), dtype=dtype, device=cache.device)
+        v = torch.empty_like(k)
+    else:
+        k, v = out
+        dtype = k.dtype
+        for name, t in (("k", k), ("v", v)):
+            if _token_rows(name, t, dev, dtype) != (T, heads, dim, heads * dim):
+                raise ValueError(f"{name} must be a contiguous {[T, heads, dim]} tensor")
+    st = (_lib or load()).qmm_kv_load(cache.data_ptr(), slots.data_ptr(), T, heads, dim, page, pages, group, code,
+                                      DTYPES[dtype], k.data_ptr(), v.data_ptr(), _stream_of(dev))
+    if st:
+        raise QmmError(st, "qmm_kv_load")
     return k, v
 
 
@@ -504,31 +560,44 @@ def kv_attend(q, cache, table, lens, cu_q=None, max_q=1, scale=None, window=0, m
     scale: None for 1 / sqrt(dim); window: 0, or how many last tokens a query
     sees; lse: fp32 [total, heads] to fill with the log-sum-exp; ws: a
     kv_workspace() (split over all SMs), or None."""
-    H, D, qstride = _token_rows("q", q, *DTYPES)
-    pages, kvh, page = _cache_shape(cache, D, mode, group)
-    _here("table", table, torch.int32)
-    if table.dim() != 2 or not table.is_contiguous():
+    dev, dtype = _cur_dev(), q.dtype
+    total, H, D, qstride = _token_rows("q", q, dev, dtype)
+    pages, kvh, page, code = _cache_shape(cache, D, mode, group, dev)
+    if table.get_device() != dev:
+        raise _bad_device("table")
+    if table.dtype is not torch.int32 or table.dim() != 2 or not table.is_contiguous():
         raise ValueError("table must be a contiguous int32 [batch, pages] tensor")
-    B, total = table.shape[0], q.shape[0]
-    _int_vector("lens", lens, B)
+    B, max_pages = table.shape
+    _int_vector("lens", lens, B, dev)
+    cu = None
     if cu_q is not None:
-        _int_vector("cu_q", cu_q, B + 1)
+        _int_vector("cu_q", cu_q, B + 1, dev)
+        cu = cu_q.data_ptr()
     if out is None:
-        out = torch.empty(total, H, D, dtype=q.dtype, device=q.device)
-    Ho, Do, ostride = _token_rows("out", out, q.dtype)
-    if (out.shape[0], Ho, Do) != (total, H, D):
-        raise ValueError("out must have q's shape")
+        out = torch.empty((total, H, D), dtype=dtype, device=q.device)
+        ostride = H * D
+    else:
+        To, Ho, Do, ostride = _token_rows("out", out, dev, dtype)
+        if To != total or Ho != H or Do != D:
+            raise ValueError("out must have q's shape")
+    lp = wp = None
+    nbytes = 0
     if lse is not None:
-        _here("lse", lse, torch.float32)
-        if tuple(lse.shape) != (total, H) or not lse.is_contiguous():
+        if lse.get_device() != dev:
+            raise _bad_device("lse")
+        if lse.dtype is not torch.float32 or tuple(lse.shape) != (total, H) or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous fp32 [total, heads] tensor")
+        lp = lse.data_ptr()
     if ws is not None:
-        _here("ws", ws)
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(load().qmm_kv_attend(_ptr(q), DTYPES[q.dtype], qstride, _ptr(cache), _ptr(table), _ptr(lens),
-                                _ptr(cu_q), B, total, max_q, H, kvh, D, page, pages, table.shape[1], group,
-                                MODES[mode], D ** -0.5 if scale is None else scale, window, _ptr(out), ostride,
-                                _ptr(lse), _ptr(ws), nbytes, _stream()), "qmm_kv_attend")
+        if ws.get_device() != dev:
+            raise _bad_device("ws")
+        wp, nbytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    st = (_lib or load()).qmm_kv_attend(q.data_ptr(), DTYPES[dtype], qstride, cache.data_ptr(), table.data_ptr(),
+                                        lens.data_ptr(), cu, B, total, max_q, H, kvh, D, page, pages, max_pages,
+                                        group, code, D ** -0.5 if scale is None else scale, window, out.data_ptr(),
+                                        ostride, lp, wp, nbytes, _stream_of(dev))
+    if st:
+        raise QmmError(st, "qmm_kv_attend")
     return out
 
 

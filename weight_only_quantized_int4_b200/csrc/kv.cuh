@@ -41,4 +41,26 @@ __host__ __device__ constexpr int kv_val_word(int dim, int n, int tok) {
   return kv_val_piece(dim, n / per, tok) * per + n % per;
 }
 
+// Nibbles (0, 4), (1, 5), (2, 6), (3, 7) of w minus the integer behind the
+// biases: bias = 1024 + z, bias16 = -(64 + z), both exact in fp16.
+__device__ __forceinline__ void decode_nibbles(uint32_t w, uint32_t bias, uint32_t bias16, uint32_t (&a)[4]) {
+  const uint32_t w8 = w >> 8;
+  a[0] = hsub2_u(lop3_and_or(w, 0x000F000Fu, 0x64006400u), bias);
+  a[1] = hfma2_u(lop3_and_or(w, 0x00F000F0u, 0x64006400u), 0x2C002C00u, bias16);
+  a[2] = hsub2_u(lop3_and_or(w8, 0x000F000Fu, 0x64006400u), bias);
+  a[3] = hfma2_u(lop3_and_or(w8, 0x00F000F0u, 0x64006400u), 0x2C002C00u, bias16);
+}
+// The biases of a pair of zero-points (fp16, integers 0 .. 15): 1024 + z and
+// -64 - z by exact fp16 additions.
+__device__ __forceinline__ void zero_biases(uint32_t z, uint32_t& bias, uint32_t& bias16) {
+  bias = hfma2_u(z, 0x3C003C00u, 0x64006400u);
+  bias16 = hfma2_u(z, 0xBC00BC00u, 0xD400D400u);
+}
+
+__device__ __forceinline__ uint32_t hmul2_u16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 }  // namespace qk

@@ -77,31 +77,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ uint32_t at_hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
-}
-
-// Nibbles (0, 4), (1, 5), (2, 6), (3, 7) of w minus the integer behind the
-// biases: bias = 1024 + z, bias16 = -(64 + z), both exact in fp16.
-__device__ __forceinline__ void decode_nibbles(uint32_t w, uint32_t bias, uint32_t bias16, uint32_t (&a)[4]) {
-  const uint32_t w8 = w >> 8;
-  a[0] = hsub2_u(lop3_and_or(w, 0x000F000Fu, 0x64006400u), bias);
-  a[1] = hfma2_u(lop3_and_or(w, 0x00F000F0u, 0x64006400u), 0x2C002C00u, bias16);
-  a[2] = hsub2_u(lop3_and_or(w8, 0x000F000Fu, 0x64006400u), bias);
-  a[3] = hfma2_u(lop3_and_or(w8, 0x00F000F0u, 0x64006400u), 0x2C002C00u, bias16);
-}
-// The biases of a pair of zero-points (fp16, integers 0 .. 15): 1024 + z and
-// -64 - z by exact fp16 additions.
-__device__ __forceinline__ void zero_biases(uint32_t z, uint32_t& bias, uint32_t& bias16) {
-  bias = hfma2_u(z, 0x3C003C00u, 0x64006400u);
-  bias16 = hfma2_u(z, 0xBC00BC00u, 0xD400D400u);
 }
 
 // What a sequence asks for.
@@ -548,7 +527,7 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
                 const uint32_t u2 = __byte_perm(vw[2 * h][w], vw[2 * h + 1][w], half ? 0x7632 : 0x5410);
                 decode_nibbles(u2, bias[h], bias16[h], d[h]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) d[h][k] = at_hmul2(d[h][k], sv[h]);
+                for (int k = 0; k < 4; ++k) d[h][k] = hmul2_u16(d[h][k], sv[h]);
               }
 #pragma unroll
               for (int e = 0; e < 2; ++e) {

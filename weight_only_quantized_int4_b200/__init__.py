@@ -288,7 +288,7 @@ def qmm_epilogue(x, qweight, scales, zeros_or_lut, N, K, mode, bits=4, group=128
     bp = rp = wp = None
     nbytes = 0
     if y is None:
-        y = torch.empty((M, N), dtype=dtype, device=x.device)
+        y = x.new_empty((M, N))
     else:
         _like_x("y", y, dev, dtype, (M, N))
     if bias is not None:
@@ -574,7 +574,7 @@ def kv_attend(q, cache, table, lens, cu_q=None, max_q=1, scale=None, window=0, m
         _int_vector("cu_q", cu_q, B + 1, dev)
         cu = cu_q.data_ptr()
     if out is None:
-        out = torch.empty((total, H, D), dtype=dtype, device=q.device)
+        out = q.new_empty((total, H, D))
         ostride = H * D
     else:
         To, Ho, Do, ostride = _token_rows("out", out, dev, dtype)

@@ -11,12 +11,18 @@
 //   S^T[16 tokens, 8 rows] = K~[16 tokens, D] . Q^T        A = decoded key codes
 //   O^T[D, 8 rows]        += V~^T[D, 16 tokens] . P^T      A = decoded value codes
 // S's accumulator fragment becomes P's operand fragment by one 8 x 8 transpose
-// in registers (movmatrix) per eight tokens.  Keys enter as the exact integers
-// q - z, their scale multiplies the fp32 sums (per group of dims); values enter
-// as fp16((q - z) s), one rounding of 2^-11; P is rounded to fp16 after a
-// factor of 2^15 that puts its range at 2^15 .. 2^-24, so a long tail of small
-// probabilities is not lost; S, m, l and O are fp32.  bf16 queries are moved to
-// fp16 by a power of two per row (exact down to 2^-28 of the row's largest).
+// in registers (movmatrix) per eight tokens.
+//
+// Codes are not decoded where the sums can do it: a nibble's bits are the fp16
+// subnormal q 2^-24 (or q 2^-20), which the tensor cores multiply exactly, so
+//   sum_d Q_d (q_d - z) s = s (2^24 S - z sum_d Q_d)           (keys, per group of dims)
+//   sum_t P_t s_t (q_t - z_t) = 2^24 O - sum_t P_t s_t z_t     (values, one scale per token)
+// with the last sum one more MMA.  Values with several groups of dims per token
+// enter as fp16((q - z) s), one rounding of 2^-11.  P (times the token's scale in
+// the first form) is rounded to fp16 once, moved by powers of two to 2^15 .. 2^-24,
+// so a long tail of small probabilities is not lost; S, m, l and O are fp32.
+// Queries are moved to fp16 by a power of two per row (exact down to 2^-25 of the
+// row's largest).
 //
 // Work split: a tile is one (sequence, key head, RT query rows); it has ceil(
 // keys / kStepTok) steps.  The steps of all tiles are divided evenly over the
@@ -38,7 +44,9 @@ constexpr int kAtThreads = kAtWarps * 32;
 constexpr int kStageTok = 32;                       // tokens per warp stage: two cache tiles
 constexpr int kStepTok = kAtWarps * kStageTok;      // tokens per CTA step
 constexpr int kAtStages = 3;
-constexpr float kPShift = 15.0f;                    // P carries 2^15
+constexpr float kLazy = 4.0f;                       // logits (base 2) may pass the reference by this
+constexpr float kPShift = 15.0f - kLazy;            // P carries 2^kPShift, at most 2^15
+constexpr int kFlush = 4;                           // stages between two flushes of O
 constexpr int kAtMaxCtasPerSm = 4;
 
 struct AtArgs {
@@ -76,6 +84,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
+}
+// D = A . B with a zero accumulator.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
@@ -123,6 +139,8 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
   constexpr int VW = D / 64;                  // value words per lane and token
   constexpr int MT = D / 16;                  // value MMA tiles
   constexpr int STAGE = 2 * TB;
+  // one scale per token: it multiplies P, and value codes enter undecoded
+  constexpr bool kFold = G == 1;
   // token at place k of the MMA's k order (and S's rows): see kv.cuh, the
   // rows read together must sit in different banks
   constexpr int SX = D == 64 ? 2 : 1;
@@ -232,57 +250,75 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
     // ---- this lane's query rows: column g of each token tile as operand,
     // columns 2t, 2t + 1 of the sums
     uint32_t qf[NT][2 * KW][2];
-    float qs[NT][2];       // scale log2(e) / (power of two of the row)
+    float qa[NT][2];       // logit (base 2) per unit of the MMA's sum
+    float qb[NT][G][2];    // logit per unit of zero-point: qa times the group's sum of q
     int hi_q[NT][2], lo_q[NT][2];
-    int full_hi = sq.len, full_lo = 0;   // tokens every row of the tile sees
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int row = rt * RT + nt * 8 + g;
       const bool ok = row < sq.rows;
       const int qi = ok ? row / a.per : 0, hq = ok ? row - qi * a.per : 0;
       const uint16_t* src = a.q + (long long)(sq.q0 + qi) * a.q_stride + (head * a.per + hq) * D;
-      float inv = a.scale_log2;
       uint4 v[KW];
 #pragma unroll
       for (int w = 0; w < KW; ++w)
         v[w] = ok ? *reinterpret_cast<const uint4*>(src + 32 * w + 8 * t) : make_uint4(0, 0, 0, 0);
-      float mul = 1.0f;
-      if (a.bf16) {
-        uint32_t top = 0;   // largest magnitude bits of the row
+      uint32_t top = 0;   // largest magnitude bits of the row
 #pragma unroll
-        for (int w = 0; w < KW; ++w)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t x = (&v[w].x)[k];
-            top = max(top, max(x & 0x7FFFu, (x >> 16) & 0x7FFFu));
-          }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^(14 - e) for the largest's exponent e, held inside fp32's normals
-        const int e = (int)(top >> 7) - 127;
-        const int k = min(max(14 - e, -126), 126);
-        mul = __int_as_float((127 + k) << 23);
-        inv *= __int_as_float((127 - k) << 23);
-      }
-#pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        uint32_t x[4];
+      for (int w = 0; w < KW; ++w)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          x[k] = (&v[w].x)[k];
-          if (a.bf16)
-            x[k] = pack2<false>(__uint_as_float(x[k] << 16) * mul, __uint_as_float(x[k] & 0xFFFF0000u) * mul);
+          const uint32_t x = (&v[w].x)[k];
+          top = max(top, max(x & 0x7FFFu, (x >> 16) & 0x7FFFu));
         }
-        // dims (p, p + 4) of the word: the pairs the decoder yields
-        qf[nt][2 * w][0] = __byte_perm(x[0], x[2], 0x5410);
-        qf[nt][2 * w][1] = __byte_perm(x[0], x[2], 0x7632);
-        qf[nt][2 * w + 1][0] = __byte_perm(x[1], x[3], 0x5410);
-        qf[nt][2 * w + 1][1] = __byte_perm(x[1], x[3], 0x7632);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // times 2^(14 - e) for the largest's exponent e, held inside fp32's normals
+      const int e = a.bf16 ? (int)(top >> 7) - 127 : (int)(top >> 10) - 15;
+      const int k2 = min(max(14 - e, -126), 126);
+      const float mul = __int_as_float((127 + k2) << 23), inv = __int_as_float((127 - k2) << 23);
+      float sum[G];
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) sum[gr] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t x = (&v[w].x)[k];
+          if (a.bf16) {
+            f[2 * k] = __uint_as_float(x << 16);
+            f[2 * k + 1] = __uint_as_float(x & 0xFFFF0000u);
+          } else {
+            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&x));
+            f[2 * k] = h.x;
+            f[2 * k + 1] = h.y;
+          }
+        }
+        // dims (p, p + 4) of the word: the pairs the code words yield; the pairs
+        // at p = 1, 3 meet codes that stand 16 times higher
+#pragma unroll
+        for (int p4 = 0; p4 < 4; ++p4) {
+          const float m2 = (p4 & 1) ? mul * 0.0625f : mul;
+          qf[nt][2 * w + (p4 >> 1)][p4 & 1] = pack2<false>(f[p4] * m2, f[p4 + 4] * m2);
+          sum[w / (GD / 32)] += f[p4] * mul + f[p4 + 4] * mul;
+        }
+      }
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
+        sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 2);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int col = 2 * t + i;
-        qs[nt][i] = __shfl_sync(0xffffffffu, inv, 4 * col);
+        const float unit = a.scale_log2 * __shfl_sync(0xffffffffu, inv, 4 * col);
+        qa[nt][i] = unit * 16777216.0f;
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+          qb[nt][gr][i] = unit * __shfl_sync(0xffffffffu, sum[gr], 4 * col);
+          if constexpr (MODE == kSYM) qb[nt][gr][i] *= 8.0f;
+        }
         const int r2 = rt * RT + nt * 8 + col;
         if (r2 < sq.rows) {
           const int pos = sq.len - sq.nq + r2 / a.per;
@@ -293,11 +329,10 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
         }
       }
     }
-    {
-      const int r0 = rt * RT, r1 = min(sq.rows, r0 + RT) - 1;
-      full_hi = sq.len - sq.nq + r0 / a.per + 1;
-      full_lo = a.window > 0 ? sq.len - sq.nq + r1 / a.per - a.window + 1 : 0;
-    }
+    // tokens every row of the tile sees
+    const int r_last = min(sq.rows, rt * RT + RT) - 1;
+    const int full_hi = sq.len - sq.nq + rt * RT / a.per + 1;
+    const int full_lo = a.window > 0 ? sq.len - sq.nq + r_last / a.per - a.window + 1 : 0;
 
     float oacc[MT][NT][4];
 #pragma unroll
@@ -306,6 +341,34 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < 4; ++k) oacc[i][nt][k] = 0.0f;
+    float cacc[kFold ? NT : 1][4];   // sum of P (SYM) or P z (ASYM), the zero-points' share of O
+#pragma unroll
+    for (int nt = 0; nt < (kFold ? NT : 1); ++nt)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) cacc[nt][k] = 0.0f;
+    // moves the zero-points' share out of O: the tensor cores truncate their sums,
+    // by up to 2^-24 of a sum of codes that are all positive, so left together O and
+    // its share drift apart (32768 tokens on one warp chain: 4e-3 of a flat row's
+    // output); taken off every kFlush stages the drift stays below 2^-12 of it
+    auto flush = [&]() {
+      if constexpr (kFold) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float z0 = cacc[nt][0] * (MODE == kSYM ? 8.0f : 1.0f), z1 = cacc[nt][1] * (MODE == kSYM ? 8.0f : 1.0f);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            // even dims' codes stand for q 2^-24, odd ones' for q 2^-20
+            oacc[mt][nt][0] = fmaf(z0, -5.9604644775390625e-8f, oacc[mt][nt][0]);
+            oacc[mt][nt][1] = fmaf(z1, -5.9604644775390625e-8f, oacc[mt][nt][1]);
+            oacc[mt][nt][2] = fmaf(z0, -9.5367431640625e-7f, oacc[mt][nt][2]);
+            oacc[mt][nt][3] = fmaf(z1, -9.5367431640625e-7f, oacc[mt][nt][3]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) cacc[nt][k] = 0.0f;
+        }
+      }
+    };
+    int vexp = 0;                    // exponent field of the largest value scale seen
     float mrow[NT][2], lrow[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -315,24 +378,330 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
         lrow[nt][i] = 0.0f;
       }
 
+    // ---- 32 tokens from a stage; FULL: every row sees all of them
+    const int tau0 = (g & 1) ? 4 + ((g >> 1) ^ SX) : (g >> 1);   // token of S's row g
+    auto compute = [&]<bool FULL>(const unsigned char* stage, int t0) {
+      // S^T = K~ Q^T: the codes are the bits of fp16 subnormals, q 2^-24 (q 2^-20
+      // for every other pair); u = logit before its token's scale
+      float u[2][NT][4], sk[2][2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const unsigned char* tp = stage + j * TB;
+        uint32_t kw[2][KW];   // rows g, g + 8
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const unsigned char* rp = tp + (tau0 + 8 * h) * KROW;
+          if constexpr (D == 64) {
+            const uint2 v = *reinterpret_cast<const uint2*>(rp + 8 * t);
+            kw[h][0] = v.x;
+            kw[h][1] = v.y;
+          } else {
+#pragma unroll
+            for (int i = 0; i < KW / 4; ++i) {
+              const int piece = (t + 4 * i) ^ (D == 256 ? 4 * (tau0 & 1) : 0);
+              const uint4 v = *reinterpret_cast<const uint4*>(rp + 16 * piece);
+              kw[h][4 * i] = v.x;
+              kw[h][4 * i + 1] = v.y;
+              kw[h][4 * i + 2] = v.z;
+              kw[h][4 * i + 3] = v.w;
+            }
+          }
+        }
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+          float sc[2], z[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const unsigned char* pp = tp + KP_OFF + ((tau0 + 8 * h) * G + gr) * PB;
+            if constexpr (MODE == kASYM) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(pp));
+              sc[h] = f.x;
+              z[h] = f.y;
+            } else {
+              sc[h] = __half2float(*reinterpret_cast<const __half*>(pp));
+              z[h] = 1.0f;   // qb holds 8 of it
+            }
+          }
+          float part[NT][4];
+#pragma unroll
+          for (int w = gr * (GD / 32); w < (gr + 1) * (GD / 32); ++w) {
+            const uint32_t w0 = kw[0][w], w1 = kw[1][w];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t y0 = half ? w0 >> 8 : w0, y1 = half ? w1 >> 8 : w1;
+              const uint32_t af[4] = {y0 & 0x000F000Fu, y1 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x00F000F0u};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (w == gr * (GD / 32) && half == 0) mma_first(part[nt], af, qf[nt][2 * w][0], qf[nt][2 * w][1]);
+                else mma_16816<false>(part[nt], af, qf[nt][2 * w + half][0], qf[nt][2 * w + half][1]);
+              }
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float v = MODE == kASYM ? fmaf(part[nt][i], qa[nt][i & 1], -z[i >> 1] * qb[nt][gr][i & 1])
+                                            : fmaf(part[nt][i], qa[nt][i & 1], -qb[nt][gr][i & 1]);
+              if constexpr (G == 1) u[j][nt][i] = v;
+              else u[j][nt][i] = gr == 0 ? sc[i >> 1] * v : fmaf(sc[i >> 1], v, u[j][nt][i]);
+            }
+          if constexpr (G == 1) {
+            sk[j][0] = sc[0];
+            sk[j][1] = sc[1];
+          } else {
+            sk[j][0] = sk[j][1] = 1.0f;
+          }
+        }
+      }
+
+      // this lane's value scales at S's rows (one scale per token): the exponent
+      // of the warp's largest keeps P times scale at the top of fp16's range
+      [[maybe_unused]] float sv[2][2];
+      if constexpr (kFold) {
+        uint32_t bits[2][2], top = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            bits[j][h] = *reinterpret_cast<const uint16_t*>(stage + j * TB + VP_OFF + (tau0 + 8 * h) * PB);
+            if constexpr (!FULL) {
+              // what lies past the sequence or before its window may be anything,
+              // and 0 times a NaN found there is a NaN: its scale reads as 0
+              const int pos = t0 + 16 * j + 8 * h + tau0;
+              if (pos >= sq.len || pos < sq.first) bits[j][h] = 0;
+            }
+            top = max(top, bits[j][h]);
+          }
+        const int e = (int)(__reduce_max_sync(0xffffffffu, top) >> 10);
+        if (e > vexp) {
+          const float f = __int_as_float((127 + max(vexp - e, -126)) << 23);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) cacc[nt][k] *= f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) oacc[mt][nt][k] *= f;
+          }
+          vexp = e;
+        }
+        const float f = __int_as_float((127 + 14 - vexp) << 23);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) sv[j][h] = __half2float(__ushort_as_half((unsigned short)bits[j][h])) * f;
+      }
+
+      // ---- running softmax: the reference m moves only when a logit exceeds it
+      // by 2^kLazy, so most stages need no maximum across lanes
+      uint32_t pf[2][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float y[2][4], most = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = G == 1 ? fmaf(u[j][nt][i], sk[j][i >> 1], -mrow[nt][i & 1]) : u[j][nt][i] - mrow[nt][i & 1];
+            if constexpr (!FULL) {
+              const int tok = t0 + 16 * j + 8 * (i >> 1) + tau0;
+              if (tok >= hi_q[nt][i & 1] || tok < lo_q[nt][i & 1]) v = -INFINITY;
+            }
+            y[j][i] = v;
+            most = fmaxf(most, v);
+          }
+        if (__any_sync(0xffffffffu, most > kLazy)) {
+#pragma unroll
+          for (int c2 = 0; c2 < 2; ++c2) {
+            float mx = mrow[nt][c2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int i = 2 * h + c2;
+                float v = G == 1 ? u[j][nt][i] * sk[j][h] : u[j][nt][i];
+                if constexpr (!FULL) {
+                  const int tok = t0 + 16 * j + 8 * h + tau0;
+                  if (tok >= hi_q[nt][c2] || tok < lo_q[nt][c2]) v = -INFINITY;
+                }
+                y[j][i] = v;
+                mx = fmaxf(mx, v);
+              }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float ref = mx == -INFINITY ? 0.0f : mx;   // nothing seen yet
+            const float alpha = exp2_fast(mrow[nt][c2] - ref);
+            mrow[nt][c2] = mx;
+            lrow[nt][c2] *= alpha;
+            if constexpr (kFold) {
+              cacc[nt][c2] *= alpha;
+              cacc[nt][2 + c2] *= alpha;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              oacc[mt][nt][c2] *= alpha;
+              oacc[mt][nt][2 + c2] *= alpha;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) y[j][2 * h + c2] -= ref;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float p0 = exp2_fast(y[j][2 * h] + kPShift), p1 = exp2_fast(y[j][2 * h + 1] + kPShift);
+            lrow[nt][0] += p0;
+            lrow[nt][1] += p1;
+            if constexpr (kFold) {
+              p0 *= sv[j][h];
+              p1 *= sv[j][h];
+            }
+            pf[j][nt][h] = transpose8x8(pack2<false>(p0, p1));
+          }
+      }
+
+      // ---- O^T += V~^T P^T
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const unsigned char* tp = stage + j * TB;
+        const int tok[4] = {t, 4 + (t ^ SX), 8 + t, 12 + (t ^ SX)};
+        uint32_t vw[4][VW];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const unsigned char* rp = tp + V_OFF + tok[k] * KROW + (D / 16) * kv_val_piece(D, g, tok[k]);
+          if constexpr (D == 64) {
+            vw[k][0] = *reinterpret_cast<const uint32_t*>(rp);
+          } else if constexpr (D == 128) {
+            const uint2 v = *reinterpret_cast<const uint2*>(rp);
+            vw[k][0] = v.x;
+            vw[k][1] = v.y;
+          } else {
+            const uint4 v = *reinterpret_cast<const uint4*>(rp);
+            vw[k][0] = v.x;
+            vw[k][1] = v.y;
+            vw[k][2] = v.z;
+            vw[k][3] = v.w;
+          }
+        }
+        uint32_t par[4] = {0, 0, 0, 0};
+        if constexpr (!kFold || MODE == kASYM) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const unsigned char* pp = tp + VP_OFF + (tok[k] * G + g * (D / 8) / GD) * PB;
+            if constexpr (MODE == kASYM) par[k] = *reinterpret_cast<const uint32_t*>(pp);
+            else par[k] = *reinterpret_cast<const uint16_t*>(pp);
+            if constexpr (!FULL) {
+              const int pos = t0 + 16 * j + tok[k];
+              if (pos >= sq.len || pos < sq.first) par[k] = 0;
+            }
+          }
+        }
+        if constexpr (kFold) {
+          // the zero-points' share: sum over tokens of P (times z), in every row
+          uint32_t zf[4];
+          if constexpr (MODE == kASYM) {
+            zf[0] = zf[1] = __byte_perm(par[0], par[1], 0x7632);
+            zf[2] = zf[3] = __byte_perm(par[2], par[3], 0x7632);
+          } else {
+            zf[0] = zf[1] = zf[2] = zf[3] = 0x3C003C00u;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_16816<false>(cacc[nt], zf, pf[j][nt][0], pf[j][nt][1]);
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {   // dims 4 half .. 4 half + 3 of the word
+              const uint32_t ab = __byte_perm(vw[0][w], vw[1][w], half ? 0x7632 : 0x5410);
+              const uint32_t cd = __byte_perm(vw[2][w], vw[3][w], half ? 0x7632 : 0x5410);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t ye = e ? ab >> 8 : ab, yf = e ? cd >> 8 : cd;
+                const uint32_t af[4] = {ye & 0x000F000Fu, ye & 0x00F000F0u, yf & 0x000F000Fu, yf & 0x00F000F0u};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_16816<false>(oacc[4 * w + 2 * half + e][nt], af, pf[j][nt][0], pf[j][nt][1]);
+              }
+            }
+          }
+        } else {
+          uint32_t sv2[2], bias[2] = {0x64086408u, 0x64086408u}, bias16[2] = {0xD480D480u, 0xD480D480u};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            sv2[h] = __byte_perm(par[2 * h], par[2 * h + 1], 0x5410);
+            if constexpr (MODE == kASYM)
+              zero_biases(__byte_perm(par[2 * h], par[2 * h + 1], 0x7632), bias[h], bias16[h]);
+          }
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t d[2][4];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t u2 = __byte_perm(vw[2 * h][w], vw[2 * h + 1][w], half ? 0x7632 : 0x5410);
+                decode_nibbles(u2, bias[h], bias16[h], d[h]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) d[h][k] = hmul2_u16(d[h][k], sv2[h]);
+              }
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t af[4] = {d[0][2 * e], d[0][2 * e + 1], d[1][2 * e], d[1][2 * e + 1]};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_16816<false>(oacc[4 * w + 2 * half + e][nt], af, pf[j][nt][0], pf[j][nt][1]);
+              }
+            }
+          }
+        }
+      }
+    };
+
     // ---- copies of this warp's 32 tokens of step s into ring stage st
     const int* trow = a.table + (long long)b * a.max_pages;
     auto token0 = [&](int s) { return sq.lo + (s * kAtWarps + warp) * kStageTok; };
+    const int pm = (1 << a.page_log2) - 1;
+    auto page_at = [&](int tt) {
+      const int id = trow[tt >> a.page_log2];
+      return (unsigned)id < (unsigned)a.pages ? id : 0;   // no access outside the cache
+    };
+    auto tile_src = [&](int id, int tt) {
+      const long long tile = (((long long)id * a.heads + head) << (a.page_log2 - 4)) + ((tt & pm) >> 4);
+      return a.cache + tile * TB + lane * 16;
+    };
+    // the page of the stage to be requested next, looked up one step ahead
+    auto page_of_step = [&](int s) {
+      const int t0 = token0(s);
+      return s < s1 && t0 < sq.len ? page_at(t0) : 0;
+    };
+    int next_page = page_of_step(s0);
     auto issue = [&](int s, int st) {
       const int t0 = token0(s);
+      const int page = next_page;
+      next_page = page_of_step(s + 1);
+      if (t0 >= sq.len) return;   // warp-uniform, as below
+      const uint32_t dst = ring_s + st * STAGE + lane * 16;
+      if (a.page_log2 > 4) {
+        // the stage's two tiles lie in one page, one after the other
+        const uint8_t* src = tile_src(page, t0);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int tt = t0 + 16 * j;
-        if (tt < sq.len) {   // warp-uniform
-          int id = trow[tt >> a.page_log2];
-          if ((unsigned)id >= (unsigned)a.pages) id = 0;   // no access outside the cache
-          const long long tile = ((long long)id * a.heads + head) * (1 << (a.page_log2 - 4)) +
-                                 ((tt & ((1 << a.page_log2) - 1)) >> 4);
-          const uint8_t* src = a.cache + tile * TB + lane * 16;
-          const uint32_t dst = ring_s + st * STAGE + j * TB + lane * 16;
+        for (int i = 0; i < STAGE / 512; ++i) at_cp16(dst + i * 512, src + i * 512);
+        if (STAGE % 512 != 0 && lane * 16 < STAGE % 512) at_cp16(dst + STAGE / 512 * 512, src + STAGE / 512 * 512);
+      } else {
 #pragma unroll
-          for (int i = 0; i < TB / 512; ++i) at_cp16(dst + i * 512, src + i * 512);
-          if (TB % 512 != 0 && lane * 16 < TB % 512) at_cp16(dst + TB / 512 * 512, src + TB / 512 * 512);
+        for (int j = 0; j < 2; ++j) {
+          const int tt = t0 + 16 * j;
+          if (tt < sq.len) {
+            const uint8_t* src = tile_src(j == 0 ? page : page_at(tt), tt);
+#pragma unroll
+            for (int i = 0; i < TB / 512; ++i) at_cp16(dst + j * TB + i * 512, src + i * 512);
+            if (TB % 512 != 0 && lane * 16 < TB % 512) at_cp16(dst + j * TB + TB / 512 * 512, src + TB / 512 * 512);
+          }
         }
       }
     };
@@ -351,200 +720,16 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
       const int t0 = token0(s);
       if (t0 < sq.len) {   // warp-uniform
         const unsigned char* stage = ring + st_c * STAGE;
-        const bool full = t0 + kStageTok <= full_hi && t0 >= full_lo;
-        const int tau0 = (g & 1) ? 4 + ((g >> 1) ^ SX) : (g >> 1);   // token of S's row g
-
-        // ---- S^T = K~ Q^T for the two 16-token tiles
-        float x[2][NT][4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const unsigned char* tp = stage + j * TB;
-          uint32_t kw[2][KW];   // rows g, g + 8
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const unsigned char* rp = tp + (tau0 + 8 * h) * KROW;
-            if constexpr (D == 64) {
-              const uint2 v = *reinterpret_cast<const uint2*>(rp + 8 * t);
-              kw[h][0] = v.x;
-              kw[h][1] = v.y;
-            } else {
-#pragma unroll
-              for (int i = 0; i < KW / 4; ++i) {
-                const int piece = (t + 4 * i) ^ (D == 256 ? 4 * (tau0 & 1) : 0);
-                const uint4 v = *reinterpret_cast<const uint4*>(rp + 16 * piece);
-                kw[h][4 * i] = v.x;
-                kw[h][4 * i + 1] = v.y;
-                kw[h][4 * i + 2] = v.z;
-                kw[h][4 * i + 3] = v.w;
-              }
-            }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[j][nt][i] = 0.0f;
-#pragma unroll
-          for (int gr = 0; gr < G; ++gr) {
-            float sc[2];
-            uint32_t bias[2] = {0x64086408u, 0x64086408u}, bias16[2] = {0xD480D480u, 0xD480D480u};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const unsigned char* pp = tp + KP_OFF + ((tau0 + 8 * h) * G + gr) * PB;
-              if constexpr (MODE == kASYM) {
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(pp);
-                sc[h] = __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu)));
-                zero_biases(__byte_perm(w, 0, 0x3232), bias[h], bias16[h]);
-              } else {
-                sc[h] = __half2float(*reinterpret_cast<const __half*>(pp));
-              }
-            }
-            float part[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) part[nt][i] = 0.0f;
-#pragma unroll
-            for (int w = gr * (GD / 32); w < (gr + 1) * (GD / 32); ++w) {
-              uint32_t d0[4], d1[4];
-              decode_nibbles(kw[0][w], bias[0], bias16[0], d0);
-              decode_nibbles(kw[1][w], bias[1], bias16[1], d1);
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const uint32_t af[4] = {d0[2 * half], d1[2 * half], d0[2 * half + 1], d1[2 * half + 1]};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  mma_16816<false>(part[nt], af, qf[nt][2 * w + half][0], qf[nt][2 * w + half][1]);
-              }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) x[j][nt][i] = fmaf(sc[i >> 1], part[nt][i], x[j][nt][i]);
-          }
-        }
-
-        // ---- running softmax
-        uint32_t pf[2][NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float alpha[2], mnew[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float mx = mrow[nt][i];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float v = x[j][nt][2 * h + i] * qs[nt][i];
-                if (!full) {
-                  const int tok = t0 + 16 * j + 8 * h + tau0;
-                  if (tok >= hi_q[nt][i] || tok < lo_q[nt][i]) v = -INFINITY;
-                }
-                x[j][nt][2 * h + i] = v;
-                mx = fmaxf(mx, v);
-              }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            mnew[i] = mx;
-            const float ref = mx == -INFINITY ? 0.0f : mx;   // nothing seen yet
-            alpha[i] = exp2_fast(mrow[nt][i] - ref);
-            float sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float p = exp2_fast(x[j][nt][2 * h + i] - ref + kPShift);
-                x[j][nt][2 * h + i] = p;
-                sum += p;
-              }
-            lrow[nt][i] = lrow[nt][i] * alpha[i] + sum;
-          }
-          if (__any_sync(0xffffffffu, mnew[0] != mrow[nt][0] || mnew[1] != mrow[nt][1])) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) oacc[mt][nt][k] *= alpha[k & 1];
-            mrow[nt][0] = mnew[0];
-            mrow[nt][1] = mnew[1];
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              pf[j][nt][h] = transpose8x8(pack2<false>(x[j][nt][2 * h], x[j][nt][2 * h + 1]));
-        }
-
-        // ---- O^T += V~^T P^T
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const unsigned char* tp = stage + j * TB;
-          int tok[4];
-          tok[0] = t;
-          tok[1] = 4 + (t ^ SX);
-          tok[2] = 8 + t;
-          tok[3] = 12 + (t ^ SX);
-          uint32_t vw[4][VW];
-          uint32_t par[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const unsigned char* rp = tp + V_OFF + tok[k] * KROW + (D / 16) * kv_val_piece(D, g, tok[k]);
-            if constexpr (D == 64) {
-              vw[k][0] = *reinterpret_cast<const uint32_t*>(rp);
-            } else if constexpr (D == 128) {
-              const uint2 v = *reinterpret_cast<const uint2*>(rp);
-              vw[k][0] = v.x;
-              vw[k][1] = v.y;
-            } else {
-              const uint4 v = *reinterpret_cast<const uint4*>(rp);
-              vw[k][0] = v.x;
-              vw[k][1] = v.y;
-              vw[k][2] = v.z;
-              vw[k][3] = v.w;
-            }
-            const unsigned char* pp = tp + VP_OFF + (tok[k] * G + g * (D / 8) / GD) * PB;
-            if constexpr (MODE == kASYM) par[k] = *reinterpret_cast<const uint32_t*>(pp);
-            else par[k] = *reinterpret_cast<const uint16_t*>(pp);
-            // what lies past the sequence or before its window may be anything,
-            // and 0 times a NaN found there is a NaN: its scale reads as 0
-            const int pos = t0 + 16 * j + tok[k];
-            if (!full && (pos >= sq.len || pos < sq.first)) par[k] = 0;
-          }
-          uint32_t sv[2], bias[2] = {0x64086408u, 0x64086408u}, bias16[2] = {0xD480D480u, 0xD480D480u};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            sv[h] = __byte_perm(par[2 * h], par[2 * h + 1], 0x5410);
-            if constexpr (MODE == kASYM)
-              zero_biases(__byte_perm(par[2 * h], par[2 * h + 1], 0x7632), bias[h], bias16[h]);
-          }
-#pragma unroll
-          for (int w = 0; w < VW; ++w) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {   // dims 4 half .. 4 half + 3 of the word
-              uint32_t d[2][4];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t u2 = __byte_perm(vw[2 * h][w], vw[2 * h + 1][w], half ? 0x7632 : 0x5410);
-                decode_nibbles(u2, bias[h], bias16[h], d[h]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) d[h][k] = hmul2_u16(d[h][k], sv[h]);
-              }
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t af[4] = {d[0][2 * e], d[0][2 * e + 1], d[1][2 * e], d[1][2 * e + 1]};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  mma_16816<false>(oacc[4 * w + 2 * half + e][nt], af, pf[j][nt][0], pf[j][nt][1]);
-              }
-            }
-          }
-        }
+        if (t0 + kStageTok <= full_hi && t0 >= full_lo) compute.template operator()<true>(stage, t0);
+        else compute.template operator()<false>(stage, t0);
       }
+      if ((s - s0) % kFlush == kFlush - 1) flush();
       __syncwarp();   // every lane is done with the stage before it is refilled
       st_c = st_c + 1 == kAtStages ? 0 : st_c + 1;
       st_f = st_f + 1 == kAtStages ? 0 : st_f + 1;
     }
     at_wait<0>();
+    flush();
 
     // ---- the warps' results through shared memory (the rings are idle)
     __syncthreads();
@@ -565,9 +750,17 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
           wl[warp * RT + row] = l;
         }
         float* dst = wo + (warp * RT + row) * D + g * (D / 8);
+        // P carried 2^(14 - vexp) of the value scales
+        float f0 = 1.0f, f1 = 1.0f;
+        if constexpr (kFold) {
+          const float f = __int_as_float((127 + vexp - 14) << 23);
+          f0 = f * 16777216.0f;
+          f1 = f * 1048576.0f;
+        }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
-          *reinterpret_cast<float2*>(dst + 2 * mt) = make_float2(oacc[mt][nt][i], oacc[mt][nt][2 + i]);
+          *reinterpret_cast<float2*>(dst + 2 * mt) =
+              make_float2(oacc[mt][nt][i] * f0, oacc[mt][nt][2 + i] * f1);
       }
     __syncthreads();
 

@@ -515,20 +515,30 @@ __global__ void __launch_bounds__(kThreads, (DEEP || NT > 2) ? 1 : 2) skinny_ker
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          float o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = acc[r][nt][i];
+          if constexpr (EPI) {
+            auto rw = [&](int i) { return (tile * R + r) * 16 + g + 8 * (i >> 1); };
+            auto tk = [&](int i) { return m_base + 8 * nt + 2 * t + (i & 1); };
+            epi_apply<BF16>(
+                a.epi, o, [&](int i) { return rw(i) < a.N && tk(i) < a.M; }, rw,
+                [&](int i) { return (size_t)tk(i) * a.N + rw(i); });
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int row = (tile * R + r) * 16 + g + 8 * (i >> 1);
             const int m = m_base + 8 * nt + 2 * t + (i & 1);
             if (row < a.N && m < a.M) {
-              float v = acc[r][nt][i];
-              if constexpr (EPI) v = epi_apply<BF16>(a.epi, v, row, (size_t)m * a.N + row);
+              const float v = o[i];
               if constexpr (BF16)
                 a.y[(size_t)m * a.N + row] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
               else
                 a.y[(size_t)m * a.N + row] = __half_as_ushort(__float2half_rn(v));
             }
           }
+        }
     }
   };
 

@@ -266,6 +266,15 @@ __device__ __forceinline__ uint32_t lut_pair(uint32_t t16, float s) {
   }
 }
 
+// A thread's 32 tokens m0 .. m0 + 31 of one weight row: the residual of a warp's
+// 32 rows is a 64-byte piece per token.
+template <bool BF16>
+__device__ __forceinline__ void epi_row(const EpiArgs& e, float (&o)[32], int row, int m0, int M, int N) {
+  epi_apply<BF16>(
+      e, o, [&](int i) { return row < N && m0 + i < M; }, [&](int) { return row; },
+      [&](int i) { return (size_t)(m0 + i) * N + row; });
+}
+
 template <int MODE, bool BF16, int BN, bool GM1, int KU, bool EPI>
 __global__ void __launch_bounds__(kTcThreads, 1)
     tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
@@ -383,13 +392,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (row < a.N)
         s_row = __half2float(__ushort_as_half(a.scales[(size_t)(row >> 4) * 16 + scale_slot(row & 15)]));
     }
-    if (EPI || !a.gated) {
+    if constexpr (EPI) {
+      float o[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = vals[i] * s_row;
+      epi_row<BF16>(a.epi, o, row, tm * BN + c0, a.M, a.N);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int m = tm * BN + c0 + i;
+        if (row < a.N && m < a.M)
+          a.y[(size_t)m * a.N + row] = BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(o[i]))
+                                            : __half_as_ushort(__float2half_rn(o[i]));
+      }
+    } else if (!a.gated) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         const int m = tm * BN + c0 + i;
         if (row < a.N && m < a.M) {
-          float o = vals[i] * s_row;
-          if constexpr (EPI) o = epi_apply<BF16>(a.epi, o, row, (size_t)m * a.N + row);
+          const float o = vals[i] * s_row;
           a.y[(size_t)m * a.N + row] = BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(o))
                                             : __half_as_ushort(__float2half_rn(o));
         }
@@ -844,14 +864,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (gissuer) bulk_wait_read_all();
         named_bar(3 + grp, 128);
       }
-      if (EPI || !a.gated) {
+      if constexpr (EPI) {
+        float o[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = vals[i] * s_row;
+        epi_row<BF16>(a.epi, o, row, tm * BN + c * 32, a.M, a.N);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          ybuf[i * kRowsTile + row_l] = BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(o[i]))
+                                             : __half_as_ushort(__float2half_rn(o[i]));
+      } else if (!a.gated) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          float o = vals[i] * s_row;
-          if constexpr (EPI) {
-            const int m = tm * BN + c * 32 + i;
-            if (row < a.N && m < a.M) o = epi_apply<BF16>(a.epi, o, row, (size_t)m * a.N + row);
-          }
+          const float o = vals[i] * s_row;
           ybuf[i * kRowsTile + row_l] = BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(o))
                                              : __half_as_ushort(__float2half_rn(o));
         }

@@ -114,13 +114,14 @@ def read_rows(cache, page_len, dim, slots, group, mode):
 
 def attend(q, keys, values, scale, window):
     """One sequence: q [m, H, dim] its last m tokens' queries, keys / values [n, KV, dim].
-    Returns (out, lse, sum_t p |v|, sum |q||k| scale) in float64."""
+    Returns float64 (out, lse, sum_t p |v|, largest sum |q||k| scale, largest step of the visible
+    values: at most a seventh of their largest magnitude, see quantize())."""
     m, H, dim = q.shape
     n, KV = keys.shape[0], keys.shape[1]
     out = np.zeros((m, H, dim))
     spread = np.zeros((m, H, dim))
     lse = np.full((m, H), -math.inf)
-    dots = np.zeros((m, H))
+    dots, step = np.zeros((m, H)), np.zeros((m, H))
     for i in range(m):
         pos = n - m + i
         first = max(0, pos - window + 1) if window else 0
@@ -134,20 +135,29 @@ def attend(q, keys, values, scale, window):
             out[i, h] = (e @ v) / e.sum()
             spread[i, h] = (e @ np.abs(v)) / e.sum()
             lse[i, h] = top + math.log(e.sum())
+            step[i, h] = np.abs(v).max() / 7 * (1 + 2.0 ** -10)
             dots[i, h] = abs(scale) * (np.abs(k) @ np.abs(q[i, h])).max()
-    return out, lse, spread, dots
+    return out, lse, spread, dots, step
 
 
-def bounds(out, spread, dots, dim, dtype):
-    """Largest error of the kernel's output and of its log-sum-exp.
+def bounds(out, spread, dots, dim, dtype, step):
+    """Largest error of the kernel's output and of its log-sum-exp.  `step`: attend()'s, for a
+    format with one scale per token, else 0.
 
     Logits: fp32 sums of at most dim + 8 exact products and their scales, and the
     exponential's argument and result, at most (dim + 16) 2^-24 + 2^-21 of the largest
     sum of magnitudes, on numerator and denominator.  Values and probabilities: one fp16
     rounding each, half a step 2^-11.  Output: half a step of its type (fp16 2^-11, bf16
     2^-8; 2^-25 absolute for fp16 below its normals).  Sums over tokens in fp32: 2^-18
-    covers 2^6 additions of halves of 2^-24 in any order of a few thousand terms."""
+    covers 2^6 additions of halves of 2^-24 in any order of a few thousand terms.
+
+    One scale per token: value codes enter the MMAs as unsigned fp16 subnormals q 2^-20, and
+    the zero-points' share is subtracted from the sums.  An MMA adds 16 products and the
+    accumulator aligned to the largest of their exponents, 24 bits kept; a subnormal counts with
+    the exponent of 2^-14, 2^6 above its unit.  So one MMA errs by at most 17 2^-24 2^6 of the
+    largest P s it adds, whatever the codes: over all MMAs at most 17 2^-18 of sum P s, which is
+    at most `step` after the division by sum P."""
     logit = (dots + 1.0) * ((dim + 16) * 2.0 ** -24 + 2.0 ** -21)
     half = 2.0 ** -11 if dtype == "f16" else 2.0 ** -8
     rel = 2 * 2.0 ** -11 * 1.01 + 2 * logit[..., None] + 2.0 ** -18
-    return rel * spread * (1 + half) + half * np.abs(out) + 2.0 ** -24, 2 * logit + 2.0 ** -18
+    return rel * spread * (1 + half) + 17 * 2.0 ** -18 * step[..., None] + half * np.abs(out) + 2.0 ** -24, 2 * logit + 2.0 ** -18

@@ -106,6 +106,10 @@ def test_store_of_values_that_are_not_finite(mode):
 
 # ------------------------------------------------------------------------ attention
 
+class Values(list):
+    one_scale = True      # of a format with one scale per token
+
+
 def _setup(lens, nq, H, KV, dim, page, mode, group, dtype, seed, qscale=1.0, spare=3):
     """A cache filled by kv_store, unwritten places left as NaN bytes; queries; the plain K~, V~."""
     rng = np.random.default_rng(seed)
@@ -120,7 +124,8 @@ def _setup(lens, nq, H, KV, dim, page, mode, group, dtype, seed, qscale=1.0, spa
         at += n
     cache = q.kv_cache(pages, KV, dim, page, mode, group)
     cache.fill_(0xFF)                                # every scale a NaN
-    keys, values = [], []
+    keys, values = [], Values()
+    values.one_scale = group in (-1, dim)
     for b, n in enumerate(lens):
         k = torch.randn(n, KV, dim, device="cuda", generator=gen).to(DT[dtype])
         v = torch.randn(n, KV, dim, device="cuda", generator=gen).to(DT[dtype])
@@ -138,12 +143,13 @@ def _setup(lens, nq, H, KV, dim, page, mode, group, dtype, seed, qscale=1.0, spa
 
 def _expect(qq, cu, keys, values, scale, window):
     parts = [plain.attend(_f64(qq[cu[b]:cu[b + 1]]), keys[b], values[b], scale, window) for b in range(len(keys))]
-    return [np.concatenate([p[i] for p in parts]) for i in range(4)]
+    o, l, spread, dots, step = (np.concatenate([p[i] for p in parts]) for i in range(5))
+    return o, l, spread, dots, step * values.one_scale
 
 
 def _check(out, lse, want, dim, dtype, what=""):
-    o, l, spread, dots = want
-    bound, lbound = plain.bounds(o, spread, dots, dim, dtype)
+    o, l, spread, dots, step = want
+    bound, lbound = plain.bounds(o, spread, dots, dim, dtype, step)
     err = np.abs(_f64(out) - o)
     assert np.all(err <= bound), (f"{what}: {int((~(err <= bound)).sum())} of {err.size} over the bound, worst "
                                   f"{np.nanmax(err / bound):.3f}, nan {int(np.isnan(err).sum())}")
@@ -240,7 +246,7 @@ def test_nan_query_stays_in_its_row():
     out = q.kv_attend(bad, cache, table, _ints(lens), scale=0.1, ws=q.kv_workspace(2, 1, 8, 1, 128))
     assert torch.isnan(out[0, 3]).all()
     keep = [h for h in range(8) if h != 3]
-    bound, _ = plain.bounds(want[0], want[2], want[3], 128, "bf16")
+    bound, _ = plain.bounds(want[0], want[2], want[3], 128, "bf16", want[4])
     err = np.abs(_f64(out) - want[0])
     assert np.all(err[1] <= bound[1]) and np.all(err[0, keep] <= bound[0, keep])
 
@@ -322,8 +328,8 @@ def test_captured_graph_serves_new_lengths():
     for new in ([50, 700], [10, 33], [0, 699]):
         ld.copy_(_ints(new))
         graph.replay()
-        want = _expect(qq, cu, [keys[b][:n] for b, n in enumerate(new)], [values[b][:n] for b, n in enumerate(new)],
-                       dim ** -0.5, 0)
+        want = _expect(qq, cu, [keys[b][:n] for b, n in enumerate(new)],
+                       Values(values[b][:n] for b, n in enumerate(new)), dim ** -0.5, 0)
         _check(out, None, want, dim, "f16", str(new))
     # a token appended inside the graph
     page = int(table[0, 10 // 16]) * 16
@@ -333,7 +339,7 @@ def test_captured_graph_serves_new_lengths():
     for x, full in ((kn, keys), (vn, values)):
         c, sc, z = plain.quantize(_f64(x), -1, "sym")
         full[0][10] = plain.decode(c, sc, z, -1)[0]
-    want = _expect(qq, cu, [keys[0][:11], keys[1][:33]], [values[0][:11], values[1][:33]], dim ** -0.5, 0)
+    want = _expect(qq, cu, [keys[0][:11], keys[1][:33]], Values([values[0][:11], values[1][:33]]), dim ** -0.5, 0)
     _check(out, None, want, dim, "f16", "appended")
 
 

@@ -16,7 +16,7 @@
 // Codes are not decoded where the sums can do it: a nibble's bits are the fp16
 // subnormal q 2^-24 (or q 2^-20), which the tensor cores multiply exactly, so
 //   sum_d Q_d (q_d - z) s = s (2^24 S - z sum_d Q_d)           (keys, per group of dims)
-//   sum_t P_t s_t (q_t - z_t) = 2^24 O - sum_t P_t s_t z_t     (values, one scale per token)
+//   sum_t P_t s_t (q_t - z_t) = 2^20 O - sum_t P_t s_t z_t     (values, one scale per token)
 // with the last sum one more MMA.  Values with several groups of dims per token
 // enter as fp16((q - z) s), one rounding of 2^-11.  P (times the token's scale in
 // the first form) is rounded to fp16 once, moved by powers of two to 2^15 .. 2^-24,
@@ -354,14 +354,15 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
       if constexpr (kFold) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float z0 = cacc[nt][0] * (MODE == kSYM ? 8.0f : 1.0f), z1 = cacc[nt][1] * (MODE == kSYM ? 8.0f : 1.0f);
+          // the codes stand for q 2^-20
+          constexpr float kUnit = (MODE == kSYM ? 8.0f : 1.0f) * 9.5367431640625e-7f;
+          const float z0 = cacc[nt][0] * kUnit, z1 = cacc[nt][1] * kUnit;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            // even dims' codes stand for q 2^-24, odd ones' for q 2^-20
-            oacc[mt][nt][0] = fmaf(z0, -5.9604644775390625e-8f, oacc[mt][nt][0]);
-            oacc[mt][nt][1] = fmaf(z1, -5.9604644775390625e-8f, oacc[mt][nt][1]);
-            oacc[mt][nt][2] = fmaf(z0, -9.5367431640625e-7f, oacc[mt][nt][2]);
-            oacc[mt][nt][3] = fmaf(z1, -9.5367431640625e-7f, oacc[mt][nt][3]);
+            oacc[mt][nt][0] -= z0;
+            oacc[mt][nt][1] -= z1;
+            oacc[mt][nt][2] -= z0;
+            oacc[mt][nt][3] -= z1;
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) cacc[nt][k] = 0.0f;
@@ -621,8 +622,10 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
               const uint32_t cd = __byte_perm(vw[2][w], vw[3][w], half ? 0x7632 : 0x5410);
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const uint32_t ye = e ? ab >> 8 : ab, yf = e ? cd >> 8 : cd;
-                const uint32_t af[4] = {ye & 0x000F000Fu, ye & 0x00F000F0u, yf & 0x000F000Fu, yf & 0x00F000F0u};
+                // all at q 2^-20, 6 bits below the operand's exponent: what the MMA
+                // cuts off the smaller of its products stays below 2^-18 of the largest
+                const uint32_t af[4] = {(e ? ab >> 4 : ab << 4) & 0x00F000F0u, (e ? ab >> 8 : ab) & 0x00F000F0u,
+                                        (e ? cd >> 4 : cd << 4) & 0x00F000F0u, (e ? cd >> 8 : cd) & 0x00F000F0u};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                   mma_16816<false>(oacc[4 * w + 2 * half + e][nt], af, pf[j][nt][0], pf[j][nt][1]);
@@ -751,16 +754,10 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
         }
         float* dst = wo + (warp * RT + row) * D + g * (D / 8);
         // P carried 2^(14 - vexp) of the value scales
-        float f0 = 1.0f, f1 = 1.0f;
-        if constexpr (kFold) {
-          const float f = __int_as_float((127 + vexp - 14) << 23);
-          f0 = f * 16777216.0f;
-          f1 = f * 1048576.0f;
-        }
+        const float f = kFold ? __int_as_float((127 + vexp - 14 + 20) << 23) : 1.0f;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
-          *reinterpret_cast<float2*>(dst + 2 * mt) =
-              make_float2(oacc[mt][nt][i] * f0, oacc[mt][nt][2 + i] * f1);
+          *reinterpret_cast<float2*>(dst + 2 * mt) = make_float2(oacc[mt][nt][i] * f, oacc[mt][nt][2 + i] * f);
       }
     __syncthreads();
 

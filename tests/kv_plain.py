@@ -140,9 +140,10 @@ def attend(q, keys, values, scale, window):
     return out, lse, spread, dots, step
 
 
-def bounds(out, spread, dots, dim, dtype, step):
+def bounds(out, spread, dots, dim, dtype, step, rounded_keys=False):
     """Largest error of the kernel's output and of its log-sum-exp.  `step`: attend()'s, for a
-    format with one scale per token, else 0.
+    format with one scale per token, else 0.  `rounded_keys`: the kernel for many rows per key
+    head takes keys as fp16((q - z) s), half a step 2^-11 off in each term of a logit.
 
     Logits: fp32 sums of at most dim + 8 exact products and their scales, and the
     exponential's argument and result, at most (dim + 16) 2^-24 + 2^-21 of the largest
@@ -158,6 +159,8 @@ def bounds(out, spread, dots, dim, dtype, step):
     largest P s it adds, whatever the codes: over all MMAs at most 17 2^-18 of sum P s, which is
     at most `step` after the division by sum P."""
     logit = (dots + 1.0) * ((dim + 16) * 2.0 ** -24 + 2.0 ** -21)
+    if rounded_keys:
+        logit = logit + 2.0 ** -11 * dots
     half = 2.0 ** -11 if dtype == "f16" else 2.0 ** -8
-    rel = 2 * 2.0 ** -11 * 1.01 + 2 * logit[..., None] + 2.0 ** -18
+    rel = 2 * 2.0 ** -11 * 1.01 + np.expm1(2 * logit)[..., None] + 2.0 ** -18
     return rel * spread * (1 + half) + 17 * 2.0 ** -18 * step[..., None] + half * np.abs(out) + 2.0 ** -24, 2 * logit + 2.0 ** -18

@@ -147,9 +147,9 @@ def _expect(qq, cu, keys, values, scale, window):
     return o, l, spread, dots, step * values.one_scale
 
 
-def _check(out, lse, want, dim, dtype, what=""):
+def _check(out, lse, want, dim, dtype, what="", rounded_keys=False):
     o, l, spread, dots, step = want
-    bound, lbound = plain.bounds(o, spread, dots, dim, dtype, step)
+    bound, lbound = plain.bounds(o, spread, dots, dim, dtype, step, rounded_keys)
     err = np.abs(_f64(out) - o)
     assert np.all(err <= bound), (f"{what}: {int((~(err <= bound)).sum())} of {err.size} over the bound, worst "
                                   f"{np.nanmax(err / bound):.3f}, nan {int(np.isnan(err).sum())}")
@@ -196,7 +196,8 @@ def test_several_queries(H, KV, nq, dim, mode, group, dtype):
             lse = torch.full((total + 2, H), 5.0, device="cuda")
             q.kv_attend(qq, cache, table, _ints(lens), cu_q=torch.tensor(cu, device="cuda"), max_q=max(nq), scale=0.11,
                         window=window, mode=mode, group=group, out=guard, lse=lse, ws=ws)
-            _check(guard[:total], lse[:total], want, dim, dtype, f"window {window} split {split}")
+            _check(guard[:total], lse[:total], want, dim, dtype, f"window {window} split {split}",
+                   rounded_keys=max(nq) * H // KV >= 64)
             assert (guard[total:] == 9.0).all() and (lse[total:] == 5.0).all()    # rows behind the last
 
 

@@ -574,7 +574,7 @@ int qmm_kv_attend(const void* q, int dtype, long long q_stride, const void* cach
   p.window = std::min(window, 1 << 30);
   p.out = out;
   p.lse = lse;
-  return status_of(launch_kv_attend(p, workspace, static_cast<cudaStream_t>(stream)));
+  return status_of(launch_kv_attend(p, workspace, wait_limit(), static_cast<cudaStream_t>(stream)));
 }
 
 long long qmm_set_wait_limit(long long cycles) {
@@ -586,8 +586,9 @@ int qmm_check_error(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return QMM_ERR_CUDA;
   const unsigned v = tc_read_and_clear_error();
   const unsigned w = skinny_read_and_clear_error();
-  if (v == 0xFFFFFFFFu || w == 0xFFFFFFFFu) return QMM_ERR_CUDA;
-  return (v | w) ? QMM_ERR_TIMEOUT : QMM_OK;
+  const unsigned k = kv_read_and_clear_error();
+  if (v == 0xFFFFFFFFu || w == 0xFFFFFFFFu || k == 0xFFFFFFFFu) return QMM_ERR_CUDA;
+  return (v | w | k) ? QMM_ERR_TIMEOUT : QMM_OK;
 }
 
 const char* qmm_strerror(int status) {

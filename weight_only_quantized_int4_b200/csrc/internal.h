@@ -126,7 +126,11 @@ struct KvAttend {
 
 size_t kv_attend_workspace(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms);
 // workspace null: no tile is split between CTAs
-cudaError_t launch_kv_attend(const KvAttend& p, void* workspace, cudaStream_t stream);
+cudaError_t launch_kv_attend(const KvAttend& p, void* workspace, long long wait_limit, cudaStream_t stream);
+// The sequences with at least min_rows query rows per key head, on the tensor
+// cores' tiles of 128 rows.
+cudaError_t launch_kv_chunk(const KvAttend& p, int min_rows, long long wait_limit, cudaStream_t stream);
+unsigned kv_read_and_clear_error();
 
 int device_sms();
 

@@ -61,6 +61,7 @@ struct AtArgs {
   unsigned* counters;   // [batch][heads][tiles_max]
   long long q_stride, out_stride;
   int batch, total_q, max_q, heads, q_heads, per, page_log2, pages, max_pages, tiles_max;
+  int rows_end;         // sequences with this many rows or more are the chunk kernel's
   float scale_log2;     // scale * log2(e)
   int window, split, bf16;
 };
@@ -119,6 +120,7 @@ __device__ __forceinline__ Seq seq_of(const AtArgs& a, int b, int RT) {
     s.nq = b < a.total_q ? 1 : 0;
   }
   s.rows = s.nq * a.per;
+  if (s.rows >= a.rows_end) s.rows = 0;
   s.tiles = (s.rows + RT - 1) / RT;
   s.first = a.window > 0 ? max(0, s.len - s.nq - a.window + 1) : 0;
   s.lo = s.first & ~(kStageTok - 1);
@@ -893,11 +895,13 @@ cudaError_t at_launch(const AtArgs& args, long long most, cudaStream_t stream) {
   return e;
 }
 
+// Sequences with at least this many query rows per key head go to the tensor-core
+// kernel (tiles of 128 rows): measured below
+constexpr int kChunkRows = 64;
+
 // Query rows per tile: 8 for a key head with up to 8 rows (and for 256 dims,
 // whose sums need the registers), else 16.
-int at_rows(int max_q, int per, int dim) {
-  return (long long)max_q * per <= 8 || dim == 256 ? 8 : 16;
-}
+int at_rows(long long most_rows, int dim) { return most_rows <= 8 || dim == 256 ? 8 : 16; }
 
 struct AtPlan {
   int rows, tiles_max, ctas;
@@ -907,8 +911,9 @@ struct AtPlan {
 AtPlan at_plan(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms) {
   AtPlan p{};
   const int per = q_heads / kv_heads;
-  p.rows = at_rows(max_q, per, dim);
-  p.tiles_max = (int)(((long long)max_q * per + p.rows - 1) / p.rows);
+  const long long most_rows = std::min<long long>((long long)max_q * per, kChunkRows - 1);
+  p.rows = at_rows(most_rows, dim);
+  p.tiles_max = (int)((most_rows + p.rows - 1) / p.rows);
   p.ctas = sms * kAtMaxCtasPerSm;
   p.counters = ((size_t)batch * kv_heads * p.tiles_max * sizeof(unsigned) + 255) / 256 * 256;
   p.slots = (size_t)2 * p.ctas * p.rows * (dim + 2) * sizeof(float);
@@ -922,8 +927,12 @@ size_t kv_attend_workspace(int batch, int max_q, int q_heads, int kv_heads, int 
   return p.counters + p.slots;
 }
 
-cudaError_t launch_kv_attend(const KvAttend& p, void* workspace, cudaStream_t stream) {
+cudaError_t launch_kv_attend(const KvAttend& p, void* workspace, long long wait_limit, cudaStream_t stream) {
   const KvCache& c = p.cache;
+  if ((long long)p.max_q * (p.q_heads / c.heads) >= kChunkRows) {
+    const cudaError_t e = launch_kv_chunk(p, kChunkRows, wait_limit, stream);
+    if (e != cudaSuccess) return e;
+  }
   const AtPlan plan = at_plan(p.batch, p.max_q, p.q_heads, c.heads, c.dim, device_sms());
   AtArgs a{};
   a.q = static_cast<const uint16_t*>(p.q);
@@ -945,6 +954,7 @@ cudaError_t launch_kv_attend(const KvAttend& p, void* workspace, cudaStream_t st
   a.pages = c.pages;
   a.max_pages = p.max_pages;
   a.tiles_max = plan.tiles_max;
+  a.rows_end = kChunkRows;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.window = p.window;
   a.bf16 = p.bf16;

@@ -70,17 +70,32 @@ struct ChCfg {
   static constexpr int O_COL = 128 * NR;                    // TMEM: S (and P) per row tile, then O
 };
 
+// Bounded wait for phase `parity` of `bar`: false (and the CTA's abort flag and the
+// error word raised) once `limit` clock cycles pass, or when another thread of the
+// CTA has given up.  The clock is read before each try, which may suspend the
+// thread for a while.
+__device__ __forceinline__ bool ch_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool ch_wait(uint64_t* bar, uint32_t parity, volatile int* abort, long long limit) {
-  if (mbar_try(bar, parity)) return true;
+  if (ch_test(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
-    if (mbar_try(bar, parity)) return true;
+    if (ch_test(bar, parity)) return true;
     if (*abort) return false;
     if (clock64() - t0 > limit) {
       *abort = 1;
       atomicOr(&g_kv_error, 1u);
       return false;
     }
+    if (mbar_try(bar, parity)) return true;
   }
 }
 
@@ -88,23 +103,34 @@ __device__ __forceinline__ uint64_t ch_desc(uint32_t saddr) {   // K-major, 128-
   return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-__device__ __forceinline__ void ch_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The MMA warp runs its loop as a whole warp, so that descriptors and addresses
+// stay in uniform registers (built by one thread they cost some 200 cycles an
+// MMA), and one elected lane (`lead`) issues.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void ch_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void ch_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void ch_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void ch_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+__device__ __forceinline__ void ch_commit(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
 }
 __device__ __forceinline__ void ch_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void ch_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -600,60 +626,67 @@ __global__ void __launch_bounds__(ChCfg<D>::THREADS, 1) kv_chunk_kernel(const Ch
   } else {
     // ------------------------------------------------------------ MMA issuer
     regs_dec<Cfg::R_MMA>();
-    if (warp == kMmaWarp && lane == 0) {
-    constexpr uint32_t kIdS = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-    constexpr uint32_t kIdO = (1u << 4) | (((uint32_t)D >> 3) << 17) | ((128u >> 4) << 24);
-    auto mma_s = [&](int r, int s) {
-      const uint32_t qa = smem_u32(sQ + r * Cfg::Q_BYTES), ka = smem_u32(sK + s * Cfg::K_BYTES);
+    if (warp == kMmaWarp) {
+      constexpr uint32_t kIdS = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+      constexpr uint32_t kIdO = (1u << 4) | (((uint32_t)D >> 3) << 17) | ((128u >> 4) << 24);
+      const uint32_t lead = elect_one();
+      // the same answer for every lane: the warp stops as one
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, ch_wait(bar, parity, abort_flag, a.wait_limit)) != 0;
+      };
+      const uint64_t dq = ch_desc(smem_u32(sQ)), dk = ch_desc(smem_u32(sK)), dv = ch_desc(smem_u32(sV));
+      // a descriptor's address field counts 16 bytes; offsets stay far inside it
+      auto mma_s = [&](int r, int s) {
+        const uint64_t qa = dq + r * (Cfg::Q_BYTES / 16), ka = dk + s * (Cfg::K_BYTES / 16);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = (k >> 2) * PANEL + 32 * (k & 3);
-        ch_mma(tmem + r * 128, ch_desc(qa + off), ch_desc(ka + off), kIdS, k > 0);
-      }
-      ch_commit(&s_full[r]);
-    };
-    bool ok = n > 0 && ch_wait(q_full, 0, abort_flag, a.wait_limit) && ch_wait(&k_full[0], 0, abort_flag, a.wait_limit);
-    if (ok) {
-      ch_after();
-#pragma unroll 1
-      for (int r = 0; r < NR; ++r) mma_s(r, 0);
-      ch_commit(&k_empty[0]);
-    }
-    // per row tile: O += P V of tile j, then S of tile j + 1, so that one row
-    // tile's softmax runs under the other's MMAs
-    for (int j = 0; ok && j < n; ++j) {
-      const int s = j % ST, s1 = (j + 1) % ST;
-      ok = ch_wait(&v_full[s], (j / ST) & 1, abort_flag, a.wait_limit);
-#pragma unroll 1
-      for (int r = 0; r < NR; ++r) {
-        ok = ok && ch_wait(&p_full[r], j & 1, abort_flag, a.wait_limit);
-        if (!ok) break;
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * (PANEL / 16) + 2 * (k & 3);
+          ch_mma(tmem + r * 128, qa + off, ka + off, kIdS, k > 0, lead);
+        }
+        ch_commit(&s_full[r], lead);
+      };
+      bool ok = n > 0 && wait(q_full, 0) && wait(&k_full[0], 0);
+      if (ok) {
         ch_after();
-        const uint32_t va = smem_u32(sV + s * Cfg::K_BYTES);
 #pragma unroll
-        for (int k = 0; k < kTok / 16; ++k)
-          ch_mma_ta(tmem + Cfg::O_COL + r * D, tmem + r * 128 + 8 * k,
-                    ch_desc(va + (k >> 2) * VPANEL + 32 * (k & 3)), kIdO, j > 0 || k > 0);
-        ch_commit(&pv_done[r]);
-        if (r == NR - 1) ch_commit(&v_empty[s]);
-        if (j + 1 < n) {
-          if (r == 0) ok = ch_wait(&k_full[s1], ((j + 1) / ST) & 1, abort_flag, a.wait_limit);
-          // P shares S's columns: the MMA that reads it must be done
-          ok = ok && ch_wait(&pv_done[r], j & 1, abort_flag, a.wait_limit);
+        for (int r = 0; r < NR; ++r) mma_s(r, 0);
+        ch_commit(&k_empty[0], lead);
+      }
+      // per row tile: O += P V of tile j, then S of tile j + 1, so that one row
+      // tile's softmax runs under the other's MMAs
+      for (int j = 0; ok && j < n; ++j) {
+        const int s = j % ST, s1 = (j + 1) % ST;
+        ok = wait(&v_full[s], (j / ST) & 1);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          ok = ok && wait(&p_full[r], j & 1);
           if (!ok) break;
           ch_after();
-          mma_s(r, s1);
-          if (r == NR - 1) ch_commit(&k_empty[s1]);
+          const uint64_t va = dv + s * (Cfg::K_BYTES / 16);
+#pragma unroll
+          for (int k = 0; k < kTok / 16; ++k)
+            ch_mma_ta(tmem + Cfg::O_COL + r * D, tmem + r * 128 + 8 * k, va + (k >> 2) * (VPANEL / 16) + 2 * (k & 3),
+                      kIdO, j > 0 || k > 0, lead);
+          ch_commit(&pv_done[r], lead);
+          if (r == NR - 1) ch_commit(&v_empty[s], lead);
+          if (j + 1 < n) {
+            if (r == 0) ok = wait(&k_full[s1], ((j + 1) / ST) & 1);
+            // P shares S's columns: the MMA that reads it must be done
+            ok = ok && wait(&pv_done[r], j & 1);
+            if (!ok) break;
+            ch_after();
+            mma_s(r, s1);
+            if (r == NR - 1) ch_commit(&k_empty[s1], lead);
+          }
         }
       }
-    }
-    // every MMA issued has finished before TMEM and the tiles are released
-    ch_commit(drain);
-    if (!mbar_try(drain, 0)) {
-      const long long c0 = clock64();
-      while (!mbar_try(drain, 0))
-        if (clock64() - c0 > kDrain) break;
-    }
+      // every MMA issued has finished before TMEM and the tiles are released
+      ch_commit(drain, lead);
+      if (!mbar_try(drain, 0)) {
+        const long long c0 = clock64();
+        while (!mbar_try(drain, 0))
+          if (clock64() - c0 > kDrain) break;
+      }
     }
   }
 

@@ -62,9 +62,9 @@ struct ChCfg {
   static constexpr int THREADS = 32 * (SOFT + kDecW + 4);    // whole warpgroups, for the register split
   // registers per thread: softmax holds a row of 128 S, decode a tile's codes; one
   // warp of each group per SM quarter, within what the launch holds (4 x 128 or 3 x 168)
-  static constexpr int R_SOFT = NR == 2 ? 192 : 208;
-  static constexpr int R_DEC = NR == 2 ? 104 : 208;
-  static constexpr int R_MMA = 24;
+  static constexpr int R_SOFT = NR == 2 ? 184 : 208;
+  static constexpr int R_DEC = NR == 2 ? 96 : 208;
+  static constexpr int R_MMA = 48;
   static_assert(NR * R_SOFT + R_DEC + R_MMA <= (NR == 2 ? 512 : 504), "register split");
   static constexpr size_t SMEM = 1024 + (size_t)NR * Q_BYTES + (size_t)ST * 2 * K_BYTES + 256;
   static constexpr int O_COL = 128 * NR;                    // TMEM: S (and P) per row tile, then O
@@ -99,9 +99,16 @@ __device__ __forceinline__ bool ch_wait(uint64_t* bar, uint32_t parity, volatile
   }
 }
 
-__device__ __forceinline__ uint64_t ch_desc(uint32_t saddr) {   // K-major, 128-byte swizzle
-  return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Shared-memory matrix descriptor (K-major, 128-byte swizzle, 8-row groups 1024
+// bytes apart): the low word holds the address in units of 16 bytes, the high one
+// is the same for every tile.
+__device__ __forceinline__ uint32_t ch_desc(uint32_t saddr) { return ((saddr >> 4) & 0x3FFF) | (1u << 16); }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+// Keeps a loop's descriptors from being computed ahead of it, all at once, in
+// registers that the MMA warp does not have.
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+  asm volatile("" : "+r"(x));
+  return x;
 }
 // The MMA warp runs its loop as a whole warp, so that descriptors and addresses
 // stay in uniform registers (built by one thread they cost some 200 cycles an
@@ -111,18 +118,20 @@ __device__ __forceinline__ uint32_t elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void ch_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
+__device__ __forceinline__ void ch_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(lead), "r"(kDescHi)
       : "memory");
 }
-__device__ __forceinline__ void ch_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
+__device__ __forceinline__ void ch_mma_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 db, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(lead), "r"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ void ch_commit(uint64_t* bar, uint32_t lead) {
@@ -634,10 +643,10 @@ __global__ void __launch_bounds__(ChCfg<D>::THREADS, 1) kv_chunk_kernel(const Ch
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, ch_wait(bar, parity, abort_flag, a.wait_limit)) != 0;
       };
-      const uint64_t dq = ch_desc(smem_u32(sQ)), dk = ch_desc(smem_u32(sK)), dv = ch_desc(smem_u32(sV));
+      const uint32_t dq = ch_desc(smem_u32(sQ)), dk = ch_desc(smem_u32(sK)), dv = ch_desc(smem_u32(sV));
       // a descriptor's address field counts 16 bytes; offsets stay far inside it
       auto mma_s = [&](int r, int s) {
-        const uint64_t qa = dq + r * (Cfg::Q_BYTES / 16), ka = dk + s * (Cfg::K_BYTES / 16);
+        const uint32_t qa = opaque(dq + r * (Cfg::Q_BYTES / 16)), ka = opaque(dk + s * (Cfg::K_BYTES / 16));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * (PANEL / 16) + 2 * (k & 3);
@@ -662,10 +671,10 @@ __global__ void __launch_bounds__(ChCfg<D>::THREADS, 1) kv_chunk_kernel(const Ch
           ok = ok && wait(&p_full[r], j & 1);
           if (!ok) break;
           ch_after();
-          const uint64_t va = dv + s * (Cfg::K_BYTES / 16);
+          const uint32_t va = opaque(dv + s * (Cfg::K_BYTES / 16)), pa = opaque(tmem + r * 128);
 #pragma unroll
           for (int k = 0; k < kTok / 16; ++k)
-            ch_mma_ta(tmem + Cfg::O_COL + r * D, tmem + r * 128 + 8 * k, va + (k >> 2) * (VPANEL / 16) + 2 * (k & 3),
+            ch_mma_ta(tmem + Cfg::O_COL + r * D, pa + 8 * k, va + (k >> 2) * (VPANEL / 16) + 2 * (k & 3),
                       kIdO, j > 0 || k > 0, lead);
           ch_commit(&pv_done[r], lead);
           if (r == NR - 1) ch_commit(&v_empty[s], lead);

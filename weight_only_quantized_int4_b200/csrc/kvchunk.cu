@@ -33,7 +33,7 @@ __device__ unsigned g_kv_error = 0;
 
 constexpr int kTok = 128;             // tokens per tile
 constexpr int kDecW = 4;              // decode warps
-constexpr float kLazy = 4.0f;         // logits (base 2) may pass the reference by this
+constexpr float kLazy = 8.0f;         // logits (base 2) may pass the reference by this
 constexpr float kPShift = 15.0f - kLazy;
 constexpr long long kDrain = 4000000000ll;   // own MMAs while draining: ~2 s
 
@@ -188,6 +188,11 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float ch_exp2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__(ChCfg<D>::THREADS, 1) kv_chunk_kernel(const Ch
       }
       float mx4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-      for (int i = 4; i < kTok; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], v[i]);
+      for (int i = 4; i < kTok; i += 2) mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], v[i], v[i + 1]);
       const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * unit;
       const bool up = mx > m + kLazy;              // always at the first visible token
       if (__any_sync(0xffffffffu, up)) {

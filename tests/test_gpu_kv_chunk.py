@@ -113,6 +113,26 @@ def test_repeats_exactly_and_without_workspace():
         assert torch.equal(o, outs[0])
 
 
+@pytest.mark.parametrize("dim,mode,group,dtype", [(128, "sym", -1, "f16"), (64, "asym", 32, "bf16"), (256, "sym", 128, "f16")])
+def test_long_sequences_are_split(dim, mode, group, dtype):
+    """Few tiles of rows on long sequences: their tokens are split between CTAs through the
+    workspace, the same way at every call; without a workspace nothing is split."""
+    lens, nq, H, KV = [4100, 130], [70, 100], 2, 1
+    cache, table, qq, cu, keys, values = _setup(lens, nq, H, KV, dim, 128, mode, group, dtype, 29)
+    total = int(cu[-1])
+    ws = q.kv_workspace(2, 100, H, KV, dim)
+    for window in (0, 2500):
+        want = _expect(qq, cu, keys, values, 0.1, window)
+        outs = []
+        for w in (ws, ws, None):
+            lse = torch.zeros(total, H, device="cuda")
+            outs.append(q.kv_attend(qq[:total], cache, table, _ints(lens), cu_q=_ints(cu), max_q=100, scale=0.1,
+                                    window=window, mode=mode, group=group, lse=lse, ws=w))
+            q.check_error()
+            _check(outs[-1], lse, want, dim, dtype, f"window {window} ws {w is not None}")
+        assert torch.equal(outs[0], outs[1])
+
+
 def test_a_wait_that_runs_out_is_reported():
     """A wait bound too short to wait for anything: the call gives up, the error is reported,
     and the next call is right."""

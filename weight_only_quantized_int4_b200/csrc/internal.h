@@ -46,8 +46,12 @@ SkinnyPlan plan_skinny(int M, int N, int K, int bits, int group, int mode, bool 
                        bool force_streamk = false);
 cudaError_t launch_skinny(const Problem& p, const SkinnyPlan& plan, void* workspace,
                           cudaStream_t stream);
-cudaError_t launch_skinny_epi(const Problem& p, const SkinnyPlan& plan, void* workspace,
-                              cudaStream_t stream);
+cudaError_t launch_skinny_epi_sym(const Problem& p, const SkinnyPlan& plan, void* workspace,
+                               cudaStream_t stream);
+cudaError_t launch_skinny_epi_asym(const Problem& p, const SkinnyPlan& plan, void* workspace,
+                               cudaStream_t stream);
+cudaError_t launch_skinny_epi_lut(const Problem& p, const SkinnyPlan& plan, void* workspace,
+                               cudaStream_t stream);
 // Decode path on the library's static scratch buffer (no allocation); sets
 // *too_large instead of launching when the problem does not fit it.
 cudaError_t launch_skinny_static(const Problem& p, int sms, cudaStream_t stream, bool* too_large);
@@ -129,7 +133,9 @@ size_t kv_attend_workspace(int batch, int max_q, int q_heads, int kv_heads, int 
 cudaError_t launch_kv_attend(const KvAttend& p, void* workspace, long long wait_limit, cudaStream_t stream);
 // The sequences with at least min_rows query rows per key head, on the tensor
 // cores' tiles of 128 rows.
-cudaError_t launch_kv_chunk(const KvAttend& p, int min_rows, long long wait_limit, cudaStream_t stream);
+cudaError_t launch_kv_chunk(const KvAttend& p, int min_rows, void* workspace, long long wait_limit,
+                            cudaStream_t stream);
+size_t kv_chunk_workspace(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms);
 unsigned kv_read_and_clear_error();
 
 int device_sms();

@@ -896,7 +896,7 @@ cudaError_t at_launch(const AtArgs& args, long long most, cudaStream_t stream) {
 }
 
 // Sequences with at least this many query rows per key head go to the tensor-core
-// kernel (tiles of 128 rows): measured below
+// kernel (tiles of 128 rows).
 constexpr int kChunkRows = 64;
 
 // Query rows per tile: 8 for a key head with up to 8 rows (and for 256 dims,
@@ -906,6 +906,7 @@ int at_rows(long long most_rows, int dim) { return most_rows <= 8 || dim == 256 
 struct AtPlan {
   int rows, tiles_max, ctas;
   size_t counters, slots;
+  size_t bytes() const { return counters + (slots + 255) / 256 * 256; }
 };
 
 AtPlan at_plan(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms) {
@@ -924,16 +925,19 @@ AtPlan at_plan(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms
 
 size_t kv_attend_workspace(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms) {
   const AtPlan p = at_plan(batch, max_q, q_heads, kv_heads, dim, sms);
-  return p.counters + p.slots;
+  const bool chunk = (long long)max_q * (q_heads / kv_heads) >= kChunkRows;
+  return p.bytes() + (chunk ? kv_chunk_workspace(batch, max_q, q_heads, kv_heads, dim, sms) : 0);
 }
 
 cudaError_t launch_kv_attend(const KvAttend& p, void* workspace, long long wait_limit, cudaStream_t stream) {
   const KvCache& c = p.cache;
+  const AtPlan plan = at_plan(p.batch, p.max_q, p.q_heads, c.heads, c.dim, device_sms());
   if ((long long)p.max_q * (p.q_heads / c.heads) >= kChunkRows) {
-    const cudaError_t e = launch_kv_chunk(p, kChunkRows, wait_limit, stream);
+    // the chunk kernel's part of the workspace follows this kernel's
+    void* rest = workspace ? static_cast<char*>(workspace) + plan.bytes() : nullptr;
+    const cudaError_t e = launch_kv_chunk(p, kChunkRows, rest, wait_limit, stream);
     if (e != cudaSuccess) return e;
   }
-  const AtPlan plan = at_plan(p.batch, p.max_q, p.q_heads, c.heads, c.dim, device_sms());
   AtArgs a{};
   a.q = static_cast<const uint16_t*>(p.q);
   a.cache = static_cast<const uint8_t*>(c.data);

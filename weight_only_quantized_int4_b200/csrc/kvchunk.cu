@@ -20,7 +20,9 @@
 // values keep their bits); S, O, the maximum and the sum are fp32.  The maximum
 // is a lazy reference: O is rescaled only when a row passes it by 2^kLazy, by the
 // softmax warps themselves, between two MMAs on it.
-// Every wait is bounded: one that runs out sets the error word and the CTA drains
+// Few tiles of rows on long sequences: a tile's tokens are split between CTAs (at
+// least kSplitTiles tiles of tokens each); each leaves O, m and l in the workspace
+// and the last to arrive adds them in order.  Every wait is bounded: one that runs out sets the error word and the CTA drains
 // its MMAs, frees TMEM and exits.
 #include <algorithm>
 
@@ -33,6 +35,8 @@ __device__ unsigned g_kv_error = 0;
 
 constexpr int kTok = 128;             // tokens per tile
 constexpr int kDecW = 4;              // decode warps
+constexpr int kSplitTiles = 8;        // tiles of tokens that are worth a CTA of their own
+constexpr int kSplitMost = 16;        // partials the last CTA adds up
 constexpr float kLazy = 8.0f;         // logits (base 2) may pass the reference by this
 constexpr float kPShift = 15.0f - kLazy;
 constexpr long long kDrain = 4000000000ll;   // own MMAs while draining: ~2 s
@@ -49,6 +53,9 @@ struct ChArgs {
   int batch, total_q, max_q, heads, q_heads, per, page_log2, pages, max_pages, tiles_max, min_rows;
   float scale_log2;
   int window, bf16;
+  int splits;           // CTAs per tile of rows
+  float* slots;         // [tiles][splits][D + 2][128 NR]: O, m, l of a part
+  unsigned* counters;   // [tiles]
 };
 
 // NR row tiles of 128 and ST stages of K~ and V~ in 227 KB and 512 TMEM columns.
@@ -67,6 +74,8 @@ struct ChCfg {
   static constexpr int R_MMA = 48;
   static_assert(NR * R_SOFT + R_DEC + R_MMA <= (NR == 2 ? 512 : 504), "register split");
   static constexpr size_t SMEM = 1024 + (size_t)NR * Q_BYTES + (size_t)ST * 2 * K_BYTES + 256;
+  static constexpr int ROWS = 128 * NR;
+  static constexpr int PART = ROWS * (D + 2);               // fp32 per partial
   static constexpr int O_COL = 128 * NR;                    // TMEM: S (and P) per row tile, then O
 };
 
@@ -140,6 +149,17 @@ __device__ __forceinline__ void ch_commit(uint64_t* bar, uint32_t lead) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
       "r"(lead)
       : "memory");
+}
+// Barrier of some warps whose result is the AND of their threads' predicates.
+__device__ __forceinline__ bool bar_and(int id, int threads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
 }
 __device__ __forceinline__ void ch_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void ch_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -228,6 +248,7 @@ __global__ void __launch_bounds__(ChCfg<D>::THREADS, 1) kv_chunk_kernel(const Ch
   uint64_t* drain = bars + 15;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* last_flag = abort_flag + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -250,8 +271,9 @@ __global__ void __launch_bounds__(ChCfg<D>::THREADS, 1) kv_chunk_kernel(const Ch
 
   // ---- this CTA's tile of rows: the last rows (which see most) first
   const int pairs = a.batch * a.heads;
-  const int rt = a.tiles_max - 1 - (int)blockIdx.x / pairs;
-  const int pr = (int)blockIdx.x % pairs;
+  const int item = (int)blockIdx.x / a.splits, part = (int)blockIdx.x - item * a.splits;
+  const int rt = a.tiles_max - 1 - item / pairs;
+  const int pr = item % pairs;
   const int b = pr / a.heads, head = pr - b * a.heads;
   const long long most = (long long)a.max_pages << a.page_log2;
   int len = a.lens[b];
@@ -273,8 +295,16 @@ __global__ void __launch_bounds__(ChCfg<D>::THREADS, 1) kv_chunk_kernel(const Ch
   const int first_seq = a.window > 0 ? max(0, base_pos - a.window + 1) : 0;
   const int hi_any = min(len, base_pos + (row_end - 1) / a.per + 1);
   const int lo_any = a.window > 0 ? max(0, base_pos + row0 / a.per - a.window + 1) : 0;
-  const int j0 = lo_any / kTok;
-  const int n = hi_any > lo_any ? (hi_any + kTok - 1) / kTok - j0 : 0;
+  int j0 = lo_any / kTok;
+  int n = hi_any > lo_any ? (hi_any + kTok - 1) / kTok - j0 : 0;
+  const int parts = min(a.splits, max(1, n / kSplitTiles));
+  if (part >= parts) return;
+  {
+    const int b0 = (int)((long long)n * part / parts), b1 = (int)((long long)n * (part + 1) / parts);
+    j0 += b0;
+    n = b1 - b0;
+  }
+  const int nr = row_end - row0 > 128 ? NR : 1;   // row tiles in use
 
   constexpr int kMmaWarp = Cfg::SOFT + kDecW;
   if (warp == kMmaWarp) {
@@ -355,7 +385,7 @@ __global__ void __launch_bounds__(ChCfg<D>::THREADS, 1) kv_chunk_kernel(const Ch
     const int full_lo = a.window > 0 ? base_pos + r_last / a.per - a.window + 1 : 0;
     float m = -INFINITY, l = 0.0f;
     bool live = true;
-    for (int j = 0; j < n; ++j) {
+    for (int j = 0; r < nr && j < n; ++j) {
       live = ch_wait(&s_full[r], j & 1, abort_flag, a.wait_limit);
       live = __all_sync(0xffffffffu, live);
       if (!live) break;
@@ -424,42 +454,108 @@ __global__ void __launch_bounds__(ChCfg<D>::THREADS, 1) kv_chunk_kernel(const Ch
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[r]);
     }
-    if (live && n > 0) {
+    if (live && n > 0 && r < nr) {
       live = ch_wait(&pv_done[r], (n - 1) & 1, abort_flag, a.wait_limit);
       live = __all_sync(0xffffffffu, live);
       ch_after();
     }
-    if (live) {
-      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-      uint16_t* dst = a.out + (long long)(q0 + qi) * a.out_stride + (long long)hq * D;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        float v[32];
-        if (n > 0) {
-          ld32_async(tO + c, v);
-          wait32(v);
-        } else {
+    auto emit = [&](int c, const float (&o)[32], float inv) {   // dims c .. c + 31 of the row
+      uint16_t* dst = a.out + (long long)(q0 + qi) * a.out_stride + (long long)hq * D + c;
+      if (ok) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-        }
-        if (ok) {
+        for (int i = 0; i < 4; ++i) {
+          uint4 w;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 o;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              // a row that sees nothing gives zeros whatever its place in TMEM holds
-              const float x0 = l == 0.0f ? 0.0f : v[8 * i + 2 * k] * inv;
-              const float x1 = l == 0.0f ? 0.0f : v[8 * i + 2 * k + 1] * inv;
-              (&o.x)[k] = a.bf16 ? pack2<true>(x0, x1) : pack2<false>(x0, x1);
-            }
-            *reinterpret_cast<uint4*>(dst + c + 8 * i) = o;
+          for (int k = 0; k < 4; ++k) {
+            // a row that sees nothing gives zeros whatever its place in TMEM holds
+            const float x0 = l == 0.0f ? 0.0f : o[8 * i + 2 * k] * inv;
+            const float x1 = l == 0.0f ? 0.0f : o[8 * i + 2 * k + 1] * inv;
+            (&w.x)[k] = a.bf16 ? pack2<true>(x0, x1) : pack2<false>(x0, x1);
           }
+          *reinterpret_cast<uint4*>(dst + 8 * i) = w;
         }
       }
+    };
+    auto emit_lse = [&]() {
       if (ok && a.lse)
         a.lse[(long long)(q0 + qi) * a.q_heads + hq] =
             l == 0.0f ? -INFINITY : 0.69314718056f * (m + log2f(l) - kPShift);
+    };
+    if (parts == 1) {
+      if (live) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          if (n > 0) {
+            ld32_async(tO + c, o);
+            wait32(o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+          }
+          emit(c, o, inv);
+        }
+        emit_lse();
+      }
+    } else {
+      const int rw = r * 128 + row_l;
+      float* mine = a.slots + ((long long)item * a.splits + part) * Cfg::PART + rw;
+      if (live && r < nr) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          ld32_async(tO + c, o);
+          wait32(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) __stcg(mine + (long long)(c + i) * Cfg::ROWS, o[i]);
+        }
+        __stcg(mine + (long long)D * Cfg::ROWS, m);
+        __stcg(mine + (long long)(D + 1) * Cfg::ROWS, l);
+      }
+      // all softmax warps: a part that gave up is not counted
+      const bool all = bar_and(1, Cfg::SOFT * 32, live);
+      if (threadIdx.x == 0 && all) {
+        unsigned prev;
+        asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;" : "=r"(prev) : "l"(a.counters + item) : "memory");
+        *last_flag = prev == (unsigned)(parts - 1);
+      }
+      bar_and(1, Cfg::SOFT * 32, true);
+      if (all && *last_flag && r < nr) {
+        const float* p0 = a.slots + (long long)item * a.splits * Cfg::PART + rw;
+        float f[kSplitMost];
+        m = -INFINITY;
+        for (int k = 0; k < parts; ++k) m = fmaxf(m, __ldcg(p0 + (long long)k * Cfg::PART + (long long)D * Cfg::ROWS));
+        const float ref = m == -INFINITY ? 0.0f : m;
+        l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kSplitMost; ++k) {
+          f[k] = 0.0f;
+          if (k < parts) {
+            const float* pk = p0 + (long long)k * Cfg::PART + (long long)D * Cfg::ROWS;
+            f[k] = ch_exp2(__ldcg(pk) - ref);
+            l += f[k] * __ldcg(pk + Cfg::ROWS);
+          }
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+#pragma unroll
+          for (int k = 0; k < kSplitMost; ++k) {
+            if (k < parts) {   // the same for every thread
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                o[i] = fmaf(f[k], __ldcg(p0 + (long long)k * Cfg::PART + (long long)(c + i) * Cfg::ROWS), o[i]);
+            }
+          }
+          emit(c, o, inv);
+        }
+        emit_lse();
+      }
+      if (threadIdx.x == 0 && all && *last_flag) a.counters[item] = 0u;   // ready for the next call
     }
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------------------ decode
@@ -663,7 +759,7 @@ __global__ void __launch_bounds__(ChCfg<D>::THREADS, 1) kv_chunk_kernel(const Ch
       if (ok) {
         ch_after();
 #pragma unroll
-        for (int r = 0; r < NR; ++r) mma_s(r, 0);
+        for (int r = 0; r < nr; ++r) mma_s(r, 0);
         ch_commit(&k_empty[0], lead);
       }
       // per row tile: O += P V of tile j, then S of tile j + 1, so that one row
@@ -672,7 +768,7 @@ __global__ void __launch_bounds__(ChCfg<D>::THREADS, 1) kv_chunk_kernel(const Ch
         const int s = j % ST, s1 = (j + 1) % ST;
         ok = wait(&v_full[s], (j / ST) & 1);
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
+        for (int r = 0; r < nr; ++r) {
           ok = ok && wait(&p_full[r], j & 1);
           if (!ok) break;
           ch_after();
@@ -682,7 +778,7 @@ __global__ void __launch_bounds__(ChCfg<D>::THREADS, 1) kv_chunk_kernel(const Ch
             ch_mma_ta(tmem + Cfg::O_COL + r * D, pa + 8 * k, va + (k >> 2) * (VPANEL / 16) + 2 * (k & 3),
                       kIdO, j > 0 || k > 0, lead);
           ch_commit(&pv_done[r], lead);
-          if (r == NR - 1) ch_commit(&v_empty[s], lead);
+          if (r == nr - 1) ch_commit(&v_empty[s], lead);
           if (j + 1 < n) {
             if (r == 0) ok = wait(&k_full[s1], ((j + 1) / ST) & 1);
             // P shares S's columns: the MMA that reads it must be done
@@ -690,7 +786,7 @@ __global__ void __launch_bounds__(ChCfg<D>::THREADS, 1) kv_chunk_kernel(const Ch
             if (!ok) break;
             ch_after();
             mma_s(r, s1);
-            if (r == NR - 1) ch_commit(&k_empty[s1], lead);
+            if (r == nr - 1) ch_commit(&k_empty[s1], lead);
           }
         }
       }
@@ -747,7 +843,36 @@ cudaError_t ch_launch(const ChArgs& args, unsigned ctas, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_kv_chunk(const KvAttend& p, int min_rows, long long wait_limit, cudaStream_t stream) {
+namespace {
+
+// Tiles of rows (upper bound) and CTAs per tile: one while the tiles alone fill
+// the SMs, else as many as do, at most kSplitMost.
+struct ChPlan {
+  int tiles_max, splits;
+  long long tiles;
+  size_t counters, bytes;
+};
+ChPlan ch_plan(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms) {
+  ChPlan p{};
+  const int rows = 128 * (dim == 256 ? 1 : 2);
+  p.tiles_max = (int)(((long long)max_q * (q_heads / kv_heads) + rows - 1) / rows);
+  p.tiles = (long long)p.tiles_max * batch * kv_heads;
+  p.splits = (int)std::max<long long>(1, std::min<long long>(kSplitMost, sms / p.tiles));
+  if (p.splits > 1) {
+    p.counters = ((size_t)p.tiles * sizeof(unsigned) + 255) / 256 * 256;
+    p.bytes = p.counters + (size_t)p.tiles * p.splits * rows * (dim + 2) * sizeof(float);
+  }
+  return p;
+}
+
+}  // namespace
+
+size_t kv_chunk_workspace(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms) {
+  return ch_plan(batch, max_q, q_heads, kv_heads, dim, sms).bytes;
+}
+
+cudaError_t launch_kv_chunk(const KvAttend& p, int min_rows, void* workspace, long long wait_limit,
+                            cudaStream_t stream) {
   const KvCache& c = p.cache;
   ChArgs a{};
   a.q = static_cast<const uint16_t*>(p.q);
@@ -773,10 +898,15 @@ cudaError_t launch_kv_chunk(const KvAttend& p, int min_rows, long long wait_limi
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.window = p.window;
   a.bf16 = p.bf16;
-  const int tile = 128 * (c.dim == 256 ? 1 : 2);
-  const long long rows = (long long)std::min(p.max_q, p.total_q) * a.per;
-  a.tiles_max = (int)((rows + tile - 1) / tile);
-  const long long ctas = (long long)a.tiles_max * p.batch * c.heads;
+  const ChPlan plan = ch_plan(p.batch, p.max_q, p.q_heads, c.heads, c.dim, device_sms());
+  a.tiles_max = plan.tiles_max;
+  a.splits = 1;
+  if (workspace && plan.splits > 1) {
+    a.splits = plan.splits;
+    a.counters = static_cast<unsigned*>(workspace);
+    a.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.counters);
+  }
+  const long long ctas = plan.tiles * a.splits;
   if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   const int gd = c.dim / c.G;
 #define CH_CASE(D, MO, GD) \

@@ -22,9 +22,9 @@ SkinnyPlan plan_skinny(int M, int N, int K, int bits, int group, int mode, bool 
   const int nsc = (K + kSC - 1) / kSC;
   const long long units = (long long)p.tiles_n * nsc;
   const int tpg = tiles_per_group(group);
-  p.smem = dispatch<true>(bits, mode, bf16, p.nt, tpg, false,
+  p.smem = dispatch<true, -1>(bits, mode, bf16, p.nt, tpg, false,
                     [&]<int B, int MO, bool BF, int T, int TP, bool D>() { return smem_bytes<B, MO, T, TP, D>(); });
-  const int occ = dispatch<true>(bits, mode, bf16, p.nt, tpg, false,
+  const int occ = dispatch<true, -1>(bits, mode, bf16, p.nt, tpg, false,
                            [&]<int B, int MO, bool BF, int T, int TP, bool D>() { return occupancy<B, MO, BF, T, TP, D, false>(); });
   // one resident wave of CTAs; every warp is a stream-K worker with >= 1 unit
   long long warps = (long long)sms * (occ > 0 ? occ : 1) * kWarps;
@@ -40,7 +40,7 @@ SkinnyPlan plan_skinny(int M, int N, int K, int bits, int group, int mode, bool 
     // deep ring (its warps' stages all requested up front on small matrices)
     if (p.tiles_n <= sms && !zero_opts(mode) && p.nt <= 2) {
       p.deep = 1;
-      p.smem = dispatch<true>(bits, mode, bf16, p.nt, tpg, true,
+      p.smem = dispatch<true, -1>(bits, mode, bf16, p.nt, tpg, true,
                         [&]<int B, int MO, bool BF, int T, int TP, bool D>() { return smem_bytes<B, MO, T, TP, D>(); });
     }
     return p;
@@ -63,8 +63,12 @@ SkinnyPlan plan_skinny(int M, int N, int K, int bits, int group, int mode, bool 
 
 cudaError_t launch_skinny(const Problem& pr, const SkinnyPlan& plan, void* workspace,
                           cudaStream_t stream) {
-  return pr.epilogue ? launch_skinny_epi(pr, plan, workspace, stream)
-                     : launch_skinny_t<false>(pr, plan, workspace, stream);
+  if (!pr.epilogue) return launch_skinny_t<false>(pr, plan, workspace, stream);
+  switch (pr.mode) {
+    case kSYM: return launch_skinny_epi_sym(pr, plan, workspace, stream);
+    case kASYM: return launch_skinny_epi_asym(pr, plan, workspace, stream);
+    default: return launch_skinny_epi_lut(pr, plan, workspace, stream);
+  }
 }
 
 }  // namespace qk

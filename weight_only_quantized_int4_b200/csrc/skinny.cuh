@@ -29,7 +29,7 @@
 //
 // EPI kernels (qmm_epilogue) end in y = residual + act(sum + bias), taken in
 // fp32 where the plain kernels round the sum.  They are compiled apart
-// (skinny_epi.cu), so the plain kernels carry nothing of it.
+// (skinny_epi_*.cu), so the plain kernels carry nothing of it.
 #pragma once
 
 #include <algorithm>
@@ -930,10 +930,13 @@ auto dispatch_tpg(int tpg, bool deep, F&& f) {
 }
 
 // ZX: the zero-point options too (the EPI kernels have the plain formats only).
-template <bool ZX, class F>
+// ONLY: the kernels of one mode (a file of its own each: they compile for minutes),
+// or -1 for all.
+template <bool ZX, int ONLY, class F>
 auto dispatch(int bits, int mode, bool bf16, int nt, int tpg, bool deep, F&& f) {
-#define QMM_CASE(B, MO, BF, T) \
-  if (bits == B && mode == MO && bf16 == BF && nt == T) return dispatch_tpg<B, MO, BF, T>(tpg, deep, f);
+#define QMM_CASE(B, MO, BF, T)          \
+  if constexpr (ONLY < 0 || ONLY == MO) \
+    if (bits == B && mode == MO && bf16 == BF && nt == T) return dispatch_tpg<B, MO, BF, T>(tpg, deep, f);
   QMM_CASE(4, kSYM, false, 1) QMM_CASE(4, kSYM, false, 2) QMM_CASE(4, kSYM, true, 1)
   QMM_CASE(4, kSYM, true, 2) QMM_CASE(4, kASYM, false, 1) QMM_CASE(4, kASYM, false, 2)
   QMM_CASE(4, kASYM, true, 1) QMM_CASE(4, kASYM, true, 2) QMM_CASE(4, kLUT, false, 1)
@@ -952,14 +955,14 @@ auto dispatch(int bits, int mode, bool bf16, int nt, int tpg, bool deep, F&& f) 
   QMM_CASE(4, kASYMQ1, false, 2) QMM_CASE(4, kASYMQ1, true, 1) QMM_CASE(4, kASYMQ1, true, 2)
   }
 #undef QMM_CASE
-  return dispatch_tpg<4, kSYM, false, 1>(tpg, deep, f);
+  return dispatch_tpg<4, ONLY < 0 ? kSYM : ONLY, false, 1>(tpg, deep, f);
 }
 
 // Tiles (of 16 columns) per group inside a 128-column stage: 8 for groups of
 // 128 columns or more (and for one group per row), else group / 16.
 int tiles_per_group(int group) { return (group == -1 || group >= kSC) ? 8 : group / 16; }
 
-template <bool EPI>
+template <bool EPI, int ONLY = -1>
 cudaError_t launch_skinny_t(const Problem& pr, const SkinnyPlan& plan, void* workspace,
                             cudaStream_t stream) {
   SkinnyArgs a{};
@@ -998,7 +1001,7 @@ cudaError_t launch_skinny_t(const Problem& pr, const SkinnyPlan& plan, void* wor
     a.slots = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + counters);
   }
   if constexpr (EPI) a.epi = epi_args(pr);
-  return dispatch<!EPI>(pr.bits, pr.mode, pr.bf16, plan.nt, tiles_per_group(pr.group), plan.deep != 0,
+  return dispatch<!EPI, ONLY>(pr.bits, pr.mode, pr.bf16, plan.nt, tiles_per_group(pr.group), plan.deep != 0,
                   [&]<int B, int MO, bool BF, int T, int TP, bool D>() {
                     a.stage_bytes = Stage<B, MO, T, TP>::BYTES;
                     return launch<B, MO, BF, T, TP, D, EPI>(a, plan.slabs, stream);

@@ -1,0 +1,11 @@
+// Decode path: the ASYM kernels that end in bias, activation and residual.
+#include "skinny.cuh"
+
+namespace qk {
+
+cudaError_t launch_skinny_epi_asym(const Problem& pr, const SkinnyPlan& plan, void* workspace,
+                               cudaStream_t stream) {
+  return launch_skinny_t<true, kASYM>(pr, plan, workspace, stream);
+}
+
+}  // namespace qk

@@ -1,0 +1,11 @@
+// Decode path: the LUT kernels that end in bias, activation and residual.
+#include "skinny.cuh"
+
+namespace qk {
+
+cudaError_t launch_skinny_epi_lut(const Problem& pr, const SkinnyPlan& plan, void* workspace,
+                               cudaStream_t stream) {
+  return launch_skinny_t<true, kLUT>(pr, plan, workspace, stream);
+}
+
+}  // namespace qk

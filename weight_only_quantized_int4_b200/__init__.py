@@ -527,7 +527,7 @@ def kv_load(cache, slots, dim, mode="sym", group=-1, dtype=torch.float16, out=No
     if out is None:
         if dtype not in DTYPES:
             raise ValueError("dtype must be fp16 or bf16")
-        k = torch.empty((T, heads, dim), dtype=dtype, device=cache.device)
+        k = cache.new_empty((T, heads, dim), dtype=dtype)
         v = torch.empty_like(k)
     else:
         k, v = out

@@ -47,7 +47,7 @@ constexpr int kAtStages = 3;
 constexpr float kLazy = 4.0f;                       // logits (base 2) may pass the reference by this
 constexpr float kPShift = 15.0f - kLazy;            // P carries 2^kPShift, at most 2^15
 constexpr int kFlush = 4;                           // stages between two flushes of O
-constexpr int kAtMaxCtasPerSm = 4;
+constexpr int kAtMaxCtasPerSm = 3;                  // (4: 128 registers, spills, and no faster)
 
 struct AtArgs {
   const uint16_t* q;
@@ -387,35 +387,55 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
       // S^T = K~ Q^T: the codes are the bits of fp16 subnormals, q 2^-24 (q 2^-20
       // for every other pair); u = logit before its token's scale
       float u[2][NT][4], sk[2][2];
+      uint32_t kw[2][2][KW];   // tile; rows g, g + 8
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const unsigned char* tp = stage + j * TB;
-        uint32_t kw[2][KW];   // rows g, g + 8
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const unsigned char* rp = tp + (tau0 + 8 * h) * KROW;
+          const unsigned char* rp = stage + j * TB + (tau0 + 8 * h) * KROW;
           if constexpr (D == 64) {
             const uint2 v = *reinterpret_cast<const uint2*>(rp + 8 * t);
-            kw[h][0] = v.x;
-            kw[h][1] = v.y;
+            kw[j][h][0] = v.x;
+            kw[j][h][1] = v.y;
           } else {
 #pragma unroll
             for (int i = 0; i < KW / 4; ++i) {
               const int piece = (t + 4 * i) ^ (D == 256 ? 4 * (tau0 & 1) : 0);
               const uint4 v = *reinterpret_cast<const uint4*>(rp + 16 * piece);
-              kw[h][4 * i] = v.x;
-              kw[h][4 * i + 1] = v.y;
-              kw[h][4 * i + 2] = v.z;
-              kw[h][4 * i + 3] = v.w;
+              kw[j][h][4 * i] = v.x;
+              kw[j][h][4 * i + 1] = v.y;
+              kw[j][h][4 * i + 2] = v.z;
+              kw[j][h][4 * i + 3] = v.w;
             }
           }
         }
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
+      for (int gr = 0; gr < G; ++gr) {
+        float part[2][NT][4];
+        // the two tiles' chains of MMAs in turn: each waits for its own last one only
+#pragma unroll
+        for (int w = gr * (GD / 32); w < (gr + 1) * (GD / 32); ++w) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t w0 = kw[j][0][w], w1 = kw[j][1][w];
+              const uint32_t y0 = half ? w0 >> 8 : w0, y1 = half ? w1 >> 8 : w1;
+              const uint32_t af[4] = {y0 & 0x000F000Fu, y1 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x00F000F0u};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (w == gr * (GD / 32) && half == 0) mma_first(part[j][nt], af, qf[nt][2 * w][0], qf[nt][2 * w][1]);
+                else mma_16816<false>(part[j][nt], af, qf[nt][2 * w + half][0], qf[nt][2 * w + half][1]);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
           float sc[2], z[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const unsigned char* pp = tp + KP_OFF + ((tau0 + 8 * h) * G + gr) * PB;
+            const unsigned char* pp = stage + j * TB + KP_OFF + ((tau0 + 8 * h) * G + gr) * PB;
             if constexpr (MODE == kASYM) {
               const float2 f = __half22float2(*reinterpret_cast<const __half2*>(pp));
               sc[h] = f.x;
@@ -425,27 +445,12 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
               z[h] = 1.0f;   // qb holds 8 of it
             }
           }
-          float part[NT][4];
-#pragma unroll
-          for (int w = gr * (GD / 32); w < (gr + 1) * (GD / 32); ++w) {
-            const uint32_t w0 = kw[0][w], w1 = kw[1][w];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const uint32_t y0 = half ? w0 >> 8 : w0, y1 = half ? w1 >> 8 : w1;
-              const uint32_t af[4] = {y0 & 0x000F000Fu, y1 & 0x000F000Fu, y0 & 0x00F000F0u, y1 & 0x00F000F0u};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                if (w == gr * (GD / 32) && half == 0) mma_first(part[nt], af, qf[nt][2 * w][0], qf[nt][2 * w][1]);
-                else mma_16816<false>(part[nt], af, qf[nt][2 * w + half][0], qf[nt][2 * w + half][1]);
-              }
-            }
-          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float v = MODE == kASYM ? fmaf(part[nt][i], qa[nt][i & 1], -z[i >> 1] * qb[nt][gr][i & 1])
-                                            : fmaf(part[nt][i], qa[nt][i & 1], -qb[nt][gr][i & 1]);
+              const float v = MODE == kASYM ? fmaf(part[j][nt][i], qa[nt][i & 1], -z[i >> 1] * qb[nt][gr][i & 1])
+                                            : fmaf(part[j][nt][i], qa[nt][i & 1], -qb[nt][gr][i & 1]);
               if constexpr (G == 1) u[j][nt][i] = v;
               else u[j][nt][i] = gr == 0 ? sc[i >> 1] * v : fmaf(sc[i >> 1], v, u[j][nt][i]);
             }
@@ -626,8 +631,9 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
               for (int e = 0; e < 2; ++e) {
                 // all at q 2^-20, 6 bits below the operand's exponent: what the MMA
                 // cuts off the smaller of its products stays below 2^-18 of the largest
-                const uint32_t af[4] = {(e ? ab >> 4 : ab << 4) & 0x00F000F0u, (e ? ab >> 8 : ab) & 0x00F000F0u,
-                                        (e ? cd >> 4 : cd << 4) & 0x00F000F0u, (e ? cd >> 8 : cd) & 0x00F000F0u};
+                const uint32_t ye = e ? ab >> 8 : ab, yf = e ? cd >> 8 : cd;
+                const uint32_t af[4] = {(ye * 16u) & 0x00F000F0u, ye & 0x00F000F0u, (yf * 16u) & 0x00F000F0u,
+                                        yf & 0x00F000F0u};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                   mma_16816<false>(oacc[4 * w + 2 * half + e][nt], af, pf[j][nt][0], pf[j][nt][1]);

@@ -43,7 +43,6 @@ constexpr int kAtWarps = 4;
 constexpr int kAtThreads = kAtWarps * 32;
 constexpr int kStageTok = 32;                       // tokens per warp stage: two cache tiles
 constexpr int kStepTok = kAtWarps * kStageTok;      // tokens per CTA step
-constexpr int kAtStages = 3;
 constexpr float kLazy = 4.0f;                       // logits (base 2) may pass the reference by this
 constexpr float kPShift = 15.0f - kLazy;            // P carries 2^kPShift, at most 2^15
 constexpr int kFlush = 4;                           // stages between two flushes of O
@@ -71,7 +70,26 @@ template <int D, int NT>
 struct AtCfg {
   static constexpr int RT = 8 * NT;
   static constexpr int PART = RT * (D + 2);   // fp32 per partial: O, m, l
+  static constexpr int CTAS = D == 256 || NT == 2 ? 2 : kAtMaxCtasPerSm;   // per SM, by registers
+  static constexpr size_t RED = (size_t)kAtWarps * PART * sizeof(float);   // the warps' results
 };
+
+// Ring depth: three stages per warp where that many CTAs then fit an SM's shared
+// memory beside the buffer of the warps' results (1 KB reserved each), else two.
+template <int D, int MODE, int GD, int NT>
+constexpr size_t at_smem(int stages) {
+  return (size_t)kAtWarps * stages * 2 * kv_tile_bytes(D, D / GD, MODE) + AtCfg<D, NT>::RED;
+}
+template <int D, int MODE, int GD, int NT>
+constexpr int at_stages() {
+  return AtCfg<D, NT>::CTAS * (at_smem<D, MODE, GD, NT>(3) + 1024) <= 228 * 1024 ? 3 : 2;
+}
+
+// 64-bit division is a long software sequence; almost every one here fits 32 bits.
+__device__ __forceinline__ long long div_pos(long long x, long long d) {
+  if ((unsigned long long)(x | d) >> 32 == 0) return (long long)((unsigned)x / (unsigned)d);
+  return x / d;
+}
 
 __device__ __forceinline__ void at_cp16(uint32_t saddr, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(saddr), "l"(src) : "memory");
@@ -129,7 +147,7 @@ __device__ __forceinline__ Seq seq_of(const AtArgs& a, int b, int RT) {
 }
 
 template <int D, int MODE, int GD, int NT>
-__global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMaxCtasPerSm)
+__global__ void __launch_bounds__(kAtThreads, AtCfg<D, NT>::CTAS)
     kv_attend_kernel(const AtArgs a) {
   constexpr int RT = AtCfg<D, NT>::RT;
   constexpr int G = D / GD;
@@ -146,11 +164,13 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
   // token at place k of the MMA's k order (and S's rows): see kv.cuh, the
   // rows read together must sit in different banks
   constexpr int SX = D == 64 ? 2 : 1;
+  constexpr int kAtStages = at_stages<D, MODE, GD, NT>();
 
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long s_scan[kAtWarps];
-  __shared__ long long s_base[2];
-  __shared__ int s_b0;
+  __shared__ long long s_scan[kAtWarps], s_scan1[kAtWarps];
+  __shared__ long long s_first;
+  __shared__ Seq s_seq;
+  __shared__ int s_b;
   __shared__ int s_last;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -161,93 +181,186 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- steps of all sequences, and this CTA's range of them
-  auto units_of = [&](int b) -> long long {
+  // ---- steps of all sequences, this CTA's range of them, and the sequence it
+  // starts in (a thread per sequence; more sequences than threads take turns)
+  auto units_of = [&](const Seq& s) { return (long long)s.tiles * a.heads * s.steps; };
+  Seq mine{};
+  long long n_mine = 0, total = 0;
+  for (int b = threadIdx.x; b < a.batch; b += kAtThreads) {
     const Seq s = seq_of(a, b, RT);
-    return (long long)s.tiles * a.heads * s.steps;
-  };
-  long long total = 0;
-  for (int b = threadIdx.x; b < a.batch; b += kAtThreads) total += units_of(b);
+    if (b == (int)threadIdx.x) {
+      mine = s;
+      n_mine = units_of(s);
+    }
+    total += units_of(s);
+  }
+  // inclusive scan of the first turn within the warp, and the total
+  long long inc = n_mine;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, inc, m);
+    if (lane >= m) inc += o;
+  }
 #pragma unroll
   for (int m = 16; m; m >>= 1) total += __shfl_xor_sync(0xffffffffu, total, m);
-  if (lane == 0) s_scan[warp] = total;
+  if (lane == 31) {
+    s_scan[warp] = total;
+    s_scan1[warp] = inc;
+  }
   __syncthreads();
   total = 0;
+  long long before = 0, first_turn = 0;
 #pragma unroll
-  for (int w = 0; w < kAtWarps; ++w) total += s_scan[w];
+  for (int w = 0; w < kAtWarps; ++w) {
+    total += s_scan[w];
+    first_turn += s_scan1[w];
+    if (w < warp) before += s_scan1[w];
+  }
   if (total == 0) return;
   const long long U = total;
   const long long C = U < (long long)gridDim.x ? U : (long long)gridDim.x;   // CTAs with work
   const long long c = blockIdx.x;
   if (c >= C) return;
-  long long u = c * U / C, u_end = (c + 1) * U / C;
-
-  // the sequence that holds unit u, and its first unit
+  long long u = div_pos(c * U, C), u_end = div_pos((c + 1) * U, C);
   {
-    long long base = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += kAtThreads) {
+    auto claim = [&](int b, const Seq& s, long long lo, long long n) {
+      if (n > 0 && lo <= u && u < lo + n) {
+        s_b = b;
+        s_first = lo;
+        s_seq = s;
+      }
+    };
+    claim(threadIdx.x, mine, before + inc - n_mine, n_mine);
+    long long base = first_turn;
+    for (int b0 = kAtThreads; b0 < a.batch && base <= u; b0 += kAtThreads) {   // the same for every thread
       const int b = b0 + threadIdx.x;
-      const long long n = b < a.batch ? units_of(b) : 0;
-      long long inc = n;
+      const Seq s = b < a.batch ? seq_of(a, b, RT) : Seq{};
+      const long long n = b < a.batch ? units_of(s) : 0;
+      long long sum = n;
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, inc, m);
-        if (lane >= m) inc += o;
+        const long long o = __shfl_up_sync(0xffffffffu, sum, m);
+        if (lane >= m) sum += o;
       }
       __syncthreads();
-      if (lane == 31) s_scan[warp] = inc;
+      if (lane == 31) s_scan[warp] = sum;
       __syncthreads();
-      long long before = base, all = base;
+      long long lo = base + sum - n;
 #pragma unroll
       for (int w = 0; w < kAtWarps; ++w) {
-        if (w < warp) before += s_scan[w];
-        all += s_scan[w];
+        if (w < warp) lo += s_scan[w];
+        base += s_scan[w];
       }
-      const long long lo = before + inc - n;
-      if (n > 0 && lo <= u && u < lo + n) {
-        s_b0 = b;
-        s_base[0] = lo;
-      }
-      base = all;
-      if (base > u) break;   // the same for every thread
+      claim(b, s, lo, n);
     }
     __syncthreads();
   }
-  int b = s_b0;
-  long long b_first = s_base[0];
-  Seq sq = seq_of(a, b, RT);
+
+  // a stretch of steps s0 .. s1 - 1 of one tile of rows
+  struct Seg {
+    Seq sq;
+    long long first;   // unit at which the sequence starts
+    int b, tile, head, rt, s0, s1;
+  };
+  Seg sg;
+  sg.b = s_b;
+  sg.first = s_first;
+  sg.sq = s_seq;
 
   if (!a.split) {
     // whole tiles only: those that start inside the range
     auto up = [&](long long v) {
-      // first tile start at or after v (v in or after sequence b)
-      int bb = b;
-      long long f = b_first;
-      Seq s = sq;
+      // first tile start at or after v (v in or after the first sequence)
+      int bb = sg.b;
+      long long f = sg.first;
+      Seq s = sg.sq;
       while (true) {
-        const long long n = (long long)s.tiles * a.heads * s.steps;
+        const long long n = units_of(s);
         if (v < f + n || bb + 1 >= a.batch) break;
         f += n;
         s = seq_of(a, ++bb, RT);
       }
-      const long long r = (v - f) % s.steps;
+      const long long r = v - f - div_pos(v - f, s.steps) * s.steps;
       return r == 0 ? v : v + s.steps - r;
     };
     const long long ub = up(u), ue = u_end >= U ? U : up(u_end);
     u = ub;
     u_end = ue;
   }
+  if (u >= u_end) return;
+
+  auto locate = [&](Seg& s) {   // the stretch that starts at unit u, in s's sequence or after it
+    while (u >= s.first + units_of(s.sq)) {
+      s.first += units_of(s.sq);
+      s.sq = seq_of(a, ++s.b, RT);
+    }
+    s.tile = (int)div_pos(u - s.first, s.sq.steps);
+    s.s0 = (int)(u - s.first - (long long)s.tile * s.sq.steps);
+    s.s1 = (int)min((long long)s.sq.steps, s.s0 + (u_end - u));
+    s.rt = s.tile / a.heads;
+    s.head = s.tile - s.rt * a.heads;
+  };
+
+  // ---- copies of this warp's 32 tokens of step s into ring stage st
+  const int pm = (1 << a.page_log2) - 1;
+  auto token0 = [&](const Seg& s, int step) { return s.sq.lo + (step * kAtWarps + warp) * kStageTok; };
+  auto page_at = [&](const Seg& s, int tt) {
+    const int id = a.table[(long long)s.b * a.max_pages + (tt >> a.page_log2)];
+    return (unsigned)id < (unsigned)a.pages ? id : 0;   // no access outside the cache
+  };
+  // the page of a step's stage, looked up a step before the copy
+  auto page_of_step = [&](const Seg& s, int step) {
+    const int t0 = token0(s, step);
+    return step < s.s1 && t0 < s.sq.len ? page_at(s, t0) : 0;
+  };
+  auto issue = [&](const Seg& s, int step, int st, int page) {
+    const int t0 = token0(s, step);
+    if (step >= s.s1 || t0 >= s.sq.len) return;   // warp-uniform, as below
+    auto tile_src = [&](int id, int tt) {
+      const long long tile = (((long long)id * a.heads + s.head) << (a.page_log2 - 4)) + ((tt & pm) >> 4);
+      return a.cache + tile * TB + lane * 16;
+    };
+    const uint32_t dst = ring_s + st * STAGE + lane * 16;
+    if (a.page_log2 > 4) {
+      // the stage's two tiles lie in one page, one after the other
+      const uint8_t* src = tile_src(page, t0);
+#pragma unroll
+      for (int i = 0; i < STAGE / 512; ++i) at_cp16(dst + i * 512, src + i * 512);
+      if (STAGE % 512 != 0 && lane * 16 < STAGE % 512) at_cp16(dst + STAGE / 512 * 512, src + STAGE / 512 * 512);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int tt = t0 + 16 * j;
+        if (tt < s.sq.len) {
+          const uint8_t* src = tile_src(j == 0 ? page : page_at(s, tt), tt);
+#pragma unroll
+          for (int i = 0; i < TB / 512; ++i) at_cp16(dst + j * TB + i * 512, src + i * 512);
+          if (TB % 512 != 0 && lane * 16 < TB % 512) at_cp16(dst + j * TB + TB / 512 * 512, src + TB / 512 * 512);
+        }
+      }
+    }
+  };
+  // a stretch's first stages: requested before the stretch before it is merged
+  int next_page;
+  auto begin = [&](const Seg& s) {
+    int page[kAtStages];
+#pragma unroll
+    for (int i = 0; i < kAtStages; ++i) page[i] = page_of_step(s, s.s0 + i);
+#pragma unroll
+    for (int i = 0; i < kAtStages - 1; ++i) {
+      issue(s, s.s0 + i, i, page[i]);
+      at_commit();
+    }
+    next_page = page[kAtStages - 1];
+  };
+
+  locate(sg);
+  begin(sg);
   bool first_seg = true;
 
-  while (u < u_end) {
-    while (u >= b_first + (long long)sq.tiles * a.heads * sq.steps) {   // next sequence with work
-      b_first += (long long)sq.tiles * a.heads * sq.steps;
-      sq = seq_of(a, ++b, RT);
-    }
-    const int tile_in = (int)((u - b_first) / sq.steps);
-    const int s0 = (int)(u - b_first - (long long)tile_in * sq.steps);
-    const int s1 = (int)min((long long)sq.steps, s0 + (u_end - u));
-    const int head = tile_in % a.heads, rt = tile_in / a.heads;
+  while (true) {
+    const Seq& sq = sg.sq;
+    const int head = sg.head, rt = sg.rt, s0 = sg.s0, s1 = sg.s1;
 
     // ---- this lane's query rows: column g of each token tile as operand,
     // columns 2t, 2t + 1 of the sums
@@ -673,62 +786,14 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
       }
     };
 
-    // ---- copies of this warp's 32 tokens of step s into ring stage st
-    const int* trow = a.table + (long long)b * a.max_pages;
-    auto token0 = [&](int s) { return sq.lo + (s * kAtWarps + warp) * kStageTok; };
-    const int pm = (1 << a.page_log2) - 1;
-    auto page_at = [&](int tt) {
-      const int id = trow[tt >> a.page_log2];
-      return (unsigned)id < (unsigned)a.pages ? id : 0;   // no access outside the cache
-    };
-    auto tile_src = [&](int id, int tt) {
-      const long long tile = (((long long)id * a.heads + head) << (a.page_log2 - 4)) + ((tt & pm) >> 4);
-      return a.cache + tile * TB + lane * 16;
-    };
-    // the page of the stage to be requested next, looked up one step ahead
-    auto page_of_step = [&](int s) {
-      const int t0 = token0(s);
-      return s < s1 && t0 < sq.len ? page_at(t0) : 0;
-    };
-    int next_page = page_of_step(s0);
-    auto issue = [&](int s, int st) {
-      const int t0 = token0(s);
-      const int page = next_page;
-      next_page = page_of_step(s + 1);
-      if (t0 >= sq.len) return;   // warp-uniform, as below
-      const uint32_t dst = ring_s + st * STAGE + lane * 16;
-      if (a.page_log2 > 4) {
-        // the stage's two tiles lie in one page, one after the other
-        const uint8_t* src = tile_src(page, t0);
-#pragma unroll
-        for (int i = 0; i < STAGE / 512; ++i) at_cp16(dst + i * 512, src + i * 512);
-        if (STAGE % 512 != 0 && lane * 16 < STAGE % 512) at_cp16(dst + STAGE / 512 * 512, src + STAGE / 512 * 512);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int tt = t0 + 16 * j;
-          if (tt < sq.len) {
-            const uint8_t* src = tile_src(j == 0 ? page : page_at(tt), tt);
-#pragma unroll
-            for (int i = 0; i < TB / 512; ++i) at_cp16(dst + j * TB + i * 512, src + i * 512);
-            if (TB % 512 != 0 && lane * 16 < TB % 512) at_cp16(dst + j * TB + TB / 512 * 512, src + TB / 512 * 512);
-          }
-        }
-      }
-    };
-
-#pragma unroll
-    for (int s = 0; s < kAtStages - 1; ++s) {
-      if (s0 + s < s1) issue(s0 + s, s);
-      at_commit();
-    }
     int st_c = 0, st_f = kAtStages - 1;
     for (int s = s0; s < s1; ++s) {
-      if (s + kAtStages - 1 < s1) issue(s + kAtStages - 1, st_f);
+      issue(sg, s + kAtStages - 1, st_f, next_page);
+      next_page = page_of_step(sg, s + kAtStages);
       at_commit();
       at_wait<kAtStages - 1>();
       __syncwarp();
-      const int t0 = token0(s);
+      const int t0 = token0(sg, s);
       if (t0 < sq.len) {   // warp-uniform
         const unsigned char* stage = ring + st_c * STAGE;
         if (t0 + kStageTok <= full_hi && t0 >= full_lo) compute.template operator()<true>(stage, t0);
@@ -742,9 +807,17 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
     at_wait<0>();
     flush();
 
-    // ---- the warps' results through shared memory (the rings are idle)
-    __syncthreads();
-    float* wm = reinterpret_cast<float*>(smem);             // [warps][RT]
+    // ---- the next stretch's first stages are on their way while this one ends
+    u += s1 - s0;
+    const bool more = u < u_end;
+    Seg next = sg;
+    if (more) {
+      locate(next);
+      begin(next);
+    }
+
+    // ---- the warps' results through shared memory
+    float* wm = reinterpret_cast<float*>(smem + kAtWarps * kAtStages * STAGE);   // [warps][RT]
     float* wl = wm + kAtWarps * RT;                         // [warps][RT]
     float* wo = wl + kAtWarps * RT;                         // [warps][RT][D]
 #pragma unroll
@@ -819,10 +892,10 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
     }
     if (!whole) {
       __syncthreads();
-      const long long t_first = b_first + (long long)tile_in * sq.steps;
-      const long long first = ((t_first + 1) * C - 1) / U;
-      const long long nb = ((t_first + sq.steps) * C - 1) / U - first + 1;
-      unsigned* counter = a.counters + ((long long)b * a.heads + head) * a.tiles_max + rt;
+      const long long t_first = sg.first + (long long)sg.tile * sq.steps;
+      const long long first = div_pos((t_first + 1) * C - 1, U);
+      const long long nb = div_pos((t_first + sq.steps) * C - 1, U) - first + 1;
+      unsigned* counter = a.counters + ((long long)sg.b * a.heads + head) * a.tiles_max + rt;
       if (threadIdx.x == 0) {
         unsigned prev;
         asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;" : "=r"(prev) : "l"(counter) : "memory");
@@ -831,7 +904,7 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
       __syncthreads();
       if (s_last) {
         // `first` left its partial in its second slot if its range began before the tile
-        const int first_e = first * U / C < t_first ? 1 : 0;
+        const int first_e = first * U < t_first * C ? 1 : 0;   // floor(first U / C) < t_first
         for (int i = threadIdx.x; i < rows_here * (D / 4); i += kAtThreads) {
           const int row = i / (D / 4), d4 = (i % (D / 4)) * 4;
           float m = -INFINITY, l = 0.0f;
@@ -855,19 +928,17 @@ __global__ void __launch_bounds__(kAtThreads, (D == 256 || NT == 2) ? 2 : kAtMax
         if (threadIdx.x == 0) *counter = 0u;   // ready for the next call
       }
     }
-    __syncthreads();   // shared memory is reused by the next tile
+    if (!more) break;
+    __syncthreads();   // the results' buffer is used again
     first_seg = false;
-    u += s1 - s0;
+    sg = next;
   }
 }
 
 template <int D, int MODE, int GD, int NT>
 cudaError_t at_launch(const AtArgs& args, long long most, cudaStream_t stream) {
   auto k = kv_attend_kernel<D, MODE, GD, NT>;
-  constexpr int RT = AtCfg<D, NT>::RT;
-  constexpr size_t ring = (size_t)kAtWarps * kAtStages * 2 * kv_tile_bytes(D, D / GD, MODE);
-  constexpr size_t red = (size_t)kAtWarps * RT * (D + 2) * sizeof(float);
-  constexpr size_t smem = ring > red ? ring : red;
+  constexpr size_t smem = at_smem<D, MODE, GD, NT>(at_stages<D, MODE, GD, NT>());
   static_assert(smem <= 227 * 1024, "shared memory of the attention kernel");
   static int occ[64] = {};   // resident CTAs per SM, once per device
   int dev = 0;

@@ -973,8 +973,19 @@ cudaError_t at_launch(const AtArgs& args, long long most, cudaStream_t stream) {
 }
 
 // Sequences with at least this many query rows per key head go to the tensor-core
-// kernel (tiles of 128 rows).
-constexpr int kChunkRows = 64;
+// kernel, which pays for tiles of 128 rows whatever they hold and splits a tile's
+// tokens only as far as SMs are left.  Measured (us, this kernel : that one, 64
+// query heads on 8 key heads, SYM, one scale per row):
+//   sequences x tokens, dim        64 rows    96 rows    128 rows
+//   1 x 32768, 128                 59 : 76    76 : 76    95 : 77
+//   8 x 4096, 128                  44 : 53    57 : 53    85 : 54
+//   8 x 32768, 128                213 : 307  277 : 303  410 : 304
+//   64 x 2048, 128                163 : 131  234 : 145  288 : 141
+//   8 x 4096, 64                   33 : 42    42 : 43    61 : 43
+//   8 x 4096, 256                  75 : 73   112 : 74   174 : 80
+int chunk_rows(int batch, int kv_heads, int dim, int sms) {
+  return dim == 256 || (long long)batch * kv_heads >= sms ? 64 : 96;
+}
 
 // Query rows per tile: 8 for a key head with up to 8 rows (and for 256 dims,
 // whose sums need the registers), else 16.
@@ -982,6 +993,8 @@ int at_rows(long long most_rows, int dim) { return most_rows <= 8 || dim == 256 
 
 struct AtPlan {
   int rows, tiles_max, ctas;
+  int chunk_rows;
+  bool chunk;       // a sequence may have that many rows
   size_t counters, slots;
   size_t bytes() const { return counters + (slots + 255) / 256 * 256; }
 };
@@ -989,7 +1002,9 @@ struct AtPlan {
 AtPlan at_plan(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms) {
   AtPlan p{};
   const int per = q_heads / kv_heads;
-  const long long most_rows = std::min<long long>((long long)max_q * per, kChunkRows - 1);
+  p.chunk_rows = chunk_rows(batch, kv_heads, dim, sms);
+  p.chunk = (long long)max_q * per >= p.chunk_rows;
+  const long long most_rows = std::min<long long>((long long)max_q * per, p.chunk_rows - 1);
   p.rows = at_rows(most_rows, dim);
   p.tiles_max = (int)((most_rows + p.rows - 1) / p.rows);
   p.ctas = sms * kAtMaxCtasPerSm;
@@ -1002,17 +1017,16 @@ AtPlan at_plan(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms
 
 size_t kv_attend_workspace(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms) {
   const AtPlan p = at_plan(batch, max_q, q_heads, kv_heads, dim, sms);
-  const bool chunk = (long long)max_q * (q_heads / kv_heads) >= kChunkRows;
-  return p.bytes() + (chunk ? kv_chunk_workspace(batch, max_q, q_heads, kv_heads, dim, sms) : 0);
+  return p.bytes() + (p.chunk ? kv_chunk_workspace(batch, max_q, q_heads, kv_heads, dim, sms) : 0);
 }
 
 cudaError_t launch_kv_attend(const KvAttend& p, void* workspace, long long wait_limit, cudaStream_t stream) {
   const KvCache& c = p.cache;
   const AtPlan plan = at_plan(p.batch, p.max_q, p.q_heads, c.heads, c.dim, device_sms());
-  if ((long long)p.max_q * (p.q_heads / c.heads) >= kChunkRows) {
+  if (plan.chunk) {
     // the chunk kernel's part of the workspace follows this kernel's
     void* rest = workspace ? static_cast<char*>(workspace) + plan.bytes() : nullptr;
-    const cudaError_t e = launch_kv_chunk(p, kChunkRows, rest, wait_limit, stream);
+    const cudaError_t e = launch_kv_chunk(p, plan.chunk_rows, rest, wait_limit, stream);
     if (e != cudaSuccess) return e;
   }
   AtArgs a{};
@@ -1035,7 +1049,7 @@ cudaError_t launch_kv_attend(const KvAttend& p, void* workspace, long long wait_
   a.pages = c.pages;
   a.max_pages = p.max_pages;
   a.tiles_max = plan.tiles_max;
-  a.rows_end = kChunkRows;
+  a.rows_end = plan.chunk_rows;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.window = p.window;
   a.bf16 = p.bf16;

@@ -368,17 +368,25 @@ int qmm_kv_load(const void* cache, const int32_t* slots, int tokens, int heads, 
  * of them.  cu_q NULL: one query per sequence (total_q = batch, max_q = 1).
  *   q     [total_q][q_heads][dim], out the same (strides as for k; no overlap)
  *   max_q an upper bound on the queries of a sequence; those past it get no output
+ *   scale finite, of any sign
  *   lse   fp32 [total_q][q_heads], log of the sum of exponentials, or NULL
  * A query that sees nothing (an empty sequence) gives zeros and lse -inf.  Rows of
  * out past cu_q[batch] are left as they are.  Lengths and pages are read on the
  * device, so a captured graph serves new ones; lengths are clamped to max_pages
  * pages, query ranges to total_q, and a page outside the cache reads as page 0 (no
  * access outside the buffers).  Nothing stored past a sequence's length or before
- * its window is used.  The sums, the softmax and its statistics are fp32; keys
- * enter exactly, values and probabilities with one fp16 rounding each.
- * workspace: qmm_kv_workspace_size bytes, 256-byte aligned, under the rules of
- * qmm's (zero filled once, reusable on a stream, one per concurrent call); NULL:
- * no tile of rows is split between CTAs (slower for few, long sequences). */
+ * its window is used.  The sums, the softmax and its statistics are fp32; what is
+ * rounded is rounded once to fp16: the probabilities (times the value's scale where
+ * a token has one scale), and the decoded values where it has several; sequences
+ * with 64 or more query rows per key head (96 where few key heads share the GPU)
+ * run on tcgen05, with decoded keys and values both rounded to fp16.
+ * workspace: qmm_kv_workspace_size bytes, 256-byte aligned, zero filled once; every
+ * completed call leaves its counters at zero, so calls of any shape that fits can
+ * share it on a stream (calls that run at the same time need one each).  It holds
+ * partial results: some megabytes, up to some 40 MB for few rows of many queries.
+ * NULL: no tile of rows is split between CTAs (slower for few, long sequences).
+ * Waits of the tcgen05 kernel are bounded as qmm_set_wait_limit says
+ * (qmm_check_error). */
 size_t qmm_kv_workspace_size(int batch, int max_q, int q_heads, int kv_heads, int dim);
 int qmm_kv_attend(const void* q, int dtype, long long q_stride, const void* cache, const int32_t* table,
                   const int32_t* lens, const int32_t* cu_q, int batch, int total_q, int max_q, int q_heads,
@@ -409,7 +417,7 @@ int qmm_check_error(void* stream);
  * QMM_ERR_TIMEOUT.  The default is about 2 s at B200 clocks; cycles <= 0
  * restores it.  A tiny value makes a call give up on purpose, which is how the
  * error path is tested.  Applies to calls launched afterwards, process-wide;
- * returns the previous value.  (Waits of the tensor-core path; the decode path
+ * returns the previous value.  (Waits of the tensor-core kernels; the decode path
  * waits only for its own asynchronous copies, which always complete.) */
 long long qmm_set_wait_limit(long long cycles);
 

@@ -344,6 +344,37 @@ def test_captured_graph_serves_new_lengths():
     _check(out, None, want, dim, "f16", "appended")
 
 
+def test_one_workspace_for_calls_of_all_shapes():
+    """Calls of different shapes in turn on one workspace: each leaves it ready for the next."""
+    shapes = [([5000, 4000, 3000], [1, 1, 1], 8, 2), ([6000], [70], 2, 1), ([900] * 20, [1] * 20, 16, 8),
+              ([3000], [3], 4, 4), ([5000], [2], 64, 1)]
+    sets = [(_setup(lens, nq, H, KV, 64, 64, "sym", -1, "f16", i), lens, nq, H, KV) for i, (lens, nq, H, KV) in enumerate(shapes)]
+    size = max(q.kv_workspace(len(lens), max(nq), H, KV, 64).numel() for _, lens, nq, H, KV in sets)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    first = {}
+    for turn in range(3):
+        for i, ((cache, table, qq, cu, _, _), lens, nq, H, KV) in enumerate(sets):
+            own = q.kv_workspace(len(lens), max(nq), H, KV, 64)
+            args = (qq[:sum(nq)], cache, table, _ints(lens))
+            kw = dict(cu_q=_ints(cu), max_q=max(nq))
+            if i not in first:
+                first[i] = q.kv_attend(*args, ws=own, **kw)
+            assert torch.equal(q.kv_attend(*args, ws=ws, **kw), first[i]), (turn, i)
+
+
+@pytest.mark.parametrize("H,KV", [(4, 2), (64, 1)])
+def test_queries_past_max_q_get_no_output(H, KV):
+    """... and the others keep their places in the sequence."""
+    lens, nq = [300], [9]
+    cache, table, qq, cu, keys, values = _setup(lens, nq, H, KV, 64, 16, "sym", -1, "f16", 61)
+    want = _expect(qq, cu, keys, values, 0.1, 40)
+    out = torch.full((9, H, 64), 8.0, device="cuda", dtype=torch.float16)
+    q.kv_attend(qq[:9], cache, table, _ints(lens), cu_q=_ints([0, 9]), max_q=5, scale=0.1, window=40, out=out,
+                ws=q.kv_workspace(1, 5, H, KV, 64))
+    _check(out[:5], None, tuple(w[:5] for w in want), 64, "f16", rounded_keys=5 * H // KV >= 64)
+    assert (out[5:] == 8.0).all()
+
+
 def test_two_streams_at_once():
     lens, H, KV, dim = [4000, 2500], 32, 4, 128
     cache, table, qq, cu, keys, values = _setup(lens, [1, 1], H, KV, dim, 64, "sym", -1, "bf16", 51)

@@ -78,7 +78,7 @@ def test_attend_refusals(lib):
     assert attend(batch=-1) == -1 and attend(total=-1, cu=C_) == -1 and attend(max_q=0, cu=C_) == -1
     assert attend(total=3) == -1 and attend(max_q=2) == -1         # without cu_q: one query each
     assert attend(dt=5) == -1 and attend(H=30) == -1 and attend(max_pages=0) == -1 and attend(window=-1) == -1
-    assert attend(scale=float("nan")) == -1
+    assert attend(scale=float("nan")) == -1 and attend(scale=float("inf")) == -1
     assert attend(max_pages=1 << 26) == -2
     for name in ("qp", "cache", "table", "lens", "out"):
         assert attend(**{name: None}) == -1, name

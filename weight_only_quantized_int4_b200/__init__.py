@@ -543,8 +543,8 @@ def kv_load(cache, slots, dim, mode="sym", group=-1, dtype=torch.float16, out=No
 
 
 def kv_workspace(batch, max_q, q_heads, kv_heads, dim, device="cuda"):
-    """A zero-filled workspace for kv_attend calls of up to these sizes' shape
-    (one per shape and stream, reusable)."""
+    """A zero-filled workspace for kv_attend calls of this shape; calls of any shape
+    whose own workspace is no larger can share it on a stream."""
     n = load().qmm_kv_workspace_size(batch, max_q, q_heads, kv_heads, dim)
     if n == 0:
         raise QmmError(-2, "qmm_kv_workspace_size")

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "common.cuh"
 #include "internal.h"
@@ -540,7 +541,7 @@ int qmm_kv_attend(const void* q, int dtype, long long q_stride, const void* cach
   if (batch == 0 || total_q == 0) return batch < 0 || total_q < 0 ? QMM_ERR_ARG : QMM_OK;
   st = check_attend(batch, max_q, q_heads, kv_heads, dim);
   if (st != QMM_OK) return st;
-  if (total_q < 0 || max_pages <= 0 || window < 0 || !(scale == scale)) return QMM_ERR_ARG;
+  if (total_q < 0 || max_pages <= 0 || window < 0 || !std::isfinite(scale)) return QMM_ERR_ARG;
   if (!cu_q && (total_q != batch || max_q != 1)) return QMM_ERR_ARG;   // one query per sequence
   if ((long long)max_pages * page > (1ll << 30)) return QMM_ERR_UNSUPPORTED;   // 32-bit token positions
   if (!q || !cache || !table || !lens || !out) return QMM_ERR_ARG;

@@ -132,10 +132,10 @@ size_t kv_attend_workspace(int batch, int max_q, int q_heads, int kv_heads, int 
 // workspace null: no tile is split between CTAs
 cudaError_t launch_kv_attend(const KvAttend& p, void* workspace, long long wait_limit, cudaStream_t stream);
 // The sequences with at least min_rows query rows per key head, on the tensor
-// cores' tiles of 128 rows.
-cudaError_t launch_kv_chunk(const KvAttend& p, int min_rows, void* workspace, long long wait_limit,
-                            cudaStream_t stream);
-size_t kv_chunk_workspace(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms);
+// cores' tiles of 128 rows.  counters: one per SM, zero, or null (nothing split).
+cudaError_t launch_kv_chunk(const KvAttend& p, int min_rows, unsigned* counters, float* slots,
+                            long long wait_limit, cudaStream_t stream);
+size_t kv_chunk_slots(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms);   // bytes
 unsigned kv_read_and_clear_error();
 
 int device_sms();

@@ -57,9 +57,9 @@ struct AtArgs {
   uint16_t* out;
   float* lse;
   float* slots;         // [2 * ctas][RT * (D + 2)]
-  unsigned* counters;   // [batch][heads][tiles_max]
+  unsigned* counters;   // [ctas]: arrivals at the tile whose first contributor the CTA is
   long long q_stride, out_stride;
-  int batch, total_q, max_q, heads, q_heads, per, page_log2, pages, max_pages, tiles_max;
+  int batch, total_q, max_q, heads, q_heads, per, page_log2, pages, max_pages;
   int rows_end;         // sequences with this many rows or more are the chunk kernel's
   float scale_log2;     // scale * log2(e)
   int window, split, bf16;
@@ -120,7 +120,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 // What a sequence asks for.
 struct Seq {
-  int len, q0, nq, rows, tiles, steps;
+  int len, q0, rows, tiles, steps;
+  int base;        // position of its first query (of all it has, computed or not)
   int first, lo;   // first token any of its queries sees; the same down to a stage border
 };
 
@@ -129,18 +130,21 @@ __device__ __forceinline__ Seq seq_of(const AtArgs& a, int b, int RT) {
   const long long most = (long long)a.max_pages << a.page_log2;
   const int len = a.lens[b];
   s.len = len < 0 ? 0 : (len > most ? (int)most : len);
+  int nq;
   if (a.cu_q) {
     const int e0 = a.cu_q[b], e1 = a.cu_q[b + 1];
     s.q0 = min(max(e0, 0), a.total_q);
-    s.nq = min(min(max(e1, s.q0), a.total_q) - s.q0, a.max_q);
+    nq = min(min(max(e1, s.q0), a.total_q) - s.q0, a.max_q);
+    s.base = s.len - min(max(e1, s.q0) - s.q0, 1 << 29);
   } else {
     s.q0 = b;
-    s.nq = b < a.total_q ? 1 : 0;
+    nq = b < a.total_q ? 1 : 0;
+    s.base = s.len - 1;
   }
-  s.rows = s.nq * a.per;
+  s.rows = nq * a.per;
   if (s.rows >= a.rows_end) s.rows = 0;
   s.tiles = (s.rows + RT - 1) / RT;
-  s.first = a.window > 0 ? max(0, s.len - s.nq - a.window + 1) : 0;
+  s.first = a.window > 0 ? max(0, s.base - a.window + 1) : 0;
   s.lo = s.first & ~(kStageTok - 1);
   s.steps = max(1, (s.len - s.lo + kStepTok - 1) / kStepTok);
   return s;
@@ -436,8 +440,8 @@ __global__ void __launch_bounds__(kAtThreads, AtCfg<D, NT>::CTAS)
         }
         const int r2 = rt * RT + nt * 8 + col;
         if (r2 < sq.rows) {
-          const int pos = sq.len - sq.nq + r2 / a.per;
-          hi_q[nt][i] = pos + 1;
+          const int pos = sq.base + r2 / a.per;
+          hi_q[nt][i] = min(pos + 1, sq.len);
           lo_q[nt][i] = a.window > 0 ? pos - a.window + 1 : 0;
         } else {
           hi_q[nt][i] = lo_q[nt][i] = 0;
@@ -446,8 +450,8 @@ __global__ void __launch_bounds__(kAtThreads, AtCfg<D, NT>::CTAS)
     }
     // tokens every row of the tile sees
     const int r_last = min(sq.rows, rt * RT + RT) - 1;
-    const int full_hi = sq.len - sq.nq + rt * RT / a.per + 1;
-    const int full_lo = a.window > 0 ? sq.len - sq.nq + r_last / a.per - a.window + 1 : 0;
+    const int full_hi = min(sq.len, sq.base + rt * RT / a.per + 1);
+    const int full_lo = a.window > 0 ? sq.base + r_last / a.per - a.window + 1 : 0;
 
     float oacc[MT][NT][4];
 #pragma unroll
@@ -895,7 +899,7 @@ __global__ void __launch_bounds__(kAtThreads, AtCfg<D, NT>::CTAS)
       const long long t_first = sg.first + (long long)sg.tile * sq.steps;
       const long long first = div_pos((t_first + 1) * C - 1, U);
       const long long nb = div_pos((t_first + sq.steps) * C - 1, U) - first + 1;
-      unsigned* counter = a.counters + ((long long)sg.b * a.heads + head) * a.tiles_max + rt;
+      unsigned* counter = a.counters + first;   // at most one split tile starts in a CTA's range
       if (threadIdx.x == 0) {
         unsigned prev;
         asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;" : "=r"(prev) : "l"(counter) : "memory");
@@ -995,9 +999,15 @@ struct AtPlan {
   int rows, tiles_max, ctas;
   int chunk_rows;
   bool chunk;       // a sequence may have that many rows
-  size_t counters, slots;
-  size_t bytes() const { return counters + (slots + 255) / 256 * 256; }
+  size_t slots;
 };
+
+// The workspace: arrival counters of this kernel's CTAs and of the chunk kernel's
+// tiles in a head of the same size for every shape (so that calls of different
+// shapes can share a workspace: they leave it zero), then partial results, which
+// the two kernels use one after the other.
+size_t at_counters(int sms) { return (size_t)sms * kAtMaxCtasPerSm * sizeof(unsigned); }
+size_t at_head(int sms) { return (at_counters(sms) + (size_t)sms * sizeof(unsigned) + 255) / 256 * 256; }
 
 AtPlan at_plan(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms) {
   AtPlan p{};
@@ -1008,7 +1018,6 @@ AtPlan at_plan(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms
   p.rows = at_rows(most_rows, dim);
   p.tiles_max = (int)((most_rows + p.rows - 1) / p.rows);
   p.ctas = sms * kAtMaxCtasPerSm;
-  p.counters = ((size_t)batch * kv_heads * p.tiles_max * sizeof(unsigned) + 255) / 256 * 256;
   p.slots = (size_t)2 * p.ctas * p.rows * (dim + 2) * sizeof(float);
   return p;
 }
@@ -1017,16 +1026,19 @@ AtPlan at_plan(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms
 
 size_t kv_attend_workspace(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms) {
   const AtPlan p = at_plan(batch, max_q, q_heads, kv_heads, dim, sms);
-  return p.bytes() + (p.chunk ? kv_chunk_workspace(batch, max_q, q_heads, kv_heads, dim, sms) : 0);
+  const size_t chunk = p.chunk ? kv_chunk_slots(batch, max_q, q_heads, kv_heads, dim, sms) : 0;
+  return at_head(sms) + std::max(p.slots, chunk);
 }
 
 cudaError_t launch_kv_attend(const KvAttend& p, void* workspace, long long wait_limit, cudaStream_t stream) {
   const KvCache& c = p.cache;
-  const AtPlan plan = at_plan(p.batch, p.max_q, p.q_heads, c.heads, c.dim, device_sms());
+  const int sms = device_sms();
+  const AtPlan plan = at_plan(p.batch, p.max_q, p.q_heads, c.heads, c.dim, sms);
+  unsigned* counters = static_cast<unsigned*>(workspace);
+  float* slots = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + at_head(sms)) : nullptr;
   if (plan.chunk) {
-    // the chunk kernel's part of the workspace follows this kernel's
-    void* rest = workspace ? static_cast<char*>(workspace) + plan.bytes() : nullptr;
-    const cudaError_t e = launch_kv_chunk(p, plan.chunk_rows, rest, wait_limit, stream);
+    unsigned* tiles = workspace ? counters + at_counters(sms) / sizeof(unsigned) : nullptr;
+    const cudaError_t e = launch_kv_chunk(p, plan.chunk_rows, tiles, slots, wait_limit, stream);
     if (e != cudaSuccess) return e;
   }
   AtArgs a{};
@@ -1048,15 +1060,14 @@ cudaError_t launch_kv_attend(const KvAttend& p, void* workspace, long long wait_
   a.page_log2 = c.page_log2;
   a.pages = c.pages;
   a.max_pages = p.max_pages;
-  a.tiles_max = plan.tiles_max;
   a.rows_end = plan.chunk_rows;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.window = p.window;
   a.bf16 = p.bf16;
   if (workspace) {
     a.split = 1;
-    a.counters = static_cast<unsigned*>(workspace);
-    a.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.counters);
+    a.counters = counters;
+    a.slots = slots;
   }
   // no more CTAs than steps the table could hold
   const long long steps = std::max<long long>(1, (((long long)p.max_pages << c.page_log2) + kStepTok - 1) / kStepTok);

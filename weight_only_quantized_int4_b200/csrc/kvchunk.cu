@@ -278,20 +278,21 @@ __global__ void __launch_bounds__(ChCfg<D>::THREADS, 1) kv_chunk_kernel(const Ch
   const long long most = (long long)a.max_pages << a.page_log2;
   int len = a.lens[b];
   len = len < 0 ? 0 : (len > most ? (int)most : len);
-  int q0, nq;
+  int q0, nq, base_pos;   // base_pos: position of the first of all its queries, computed or not
   if (a.cu_q) {
     const int e0 = a.cu_q[b], e1 = a.cu_q[b + 1];
     q0 = min(max(e0, 0), a.total_q);
     nq = min(min(max(e1, q0), a.total_q) - q0, a.max_q);
+    base_pos = len - min(max(e1, q0) - q0, 1 << 29);
   } else {
     q0 = b;
     nq = b < a.total_q ? 1 : 0;
+    base_pos = len - 1;
   }
   const int rows = nq * a.per;
   if (rows < a.min_rows || rt * 128 * NR >= rows) return;   // another kernel's, or none (no TMEM taken yet)
   const int row0 = rt * 128 * NR, row_end = min(rows, row0 + 128 * NR);
   // tokens any / every row of the CTA sees
-  const int base_pos = len - nq;
   const int first_seq = a.window > 0 ? max(0, base_pos - a.window + 1) : 0;
   const int hi_any = min(len, base_pos + (row_end - 1) / a.per + 1);
   const int lo_any = a.window > 0 ? max(0, base_pos + row0 / a.per - a.window + 1) : 0;
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(ChCfg<D>::THREADS, 1) kv_chunk_kernel(const Ch
     const int pos = base_pos + row / a.per;
     const int hi_q = ok ? min(len, pos + 1) : 0, lo_q = ok && a.window > 0 ? max(0, pos - a.window + 1) : 0;
     const int r_first = row0 + r * 128, r_last = min(rows, r_first + 128) - 1;
-    const int full_hi = base_pos + r_first / a.per + 1;
+    const int full_hi = min(len, base_pos + r_first / a.per + 1);
     const int full_lo = a.window > 0 ? base_pos + r_last / a.per - a.window + 1 : 0;
     float m = -INFINITY, l = 0.0f;
     bool live = true;
@@ -850,7 +851,7 @@ namespace {
 struct ChPlan {
   int tiles_max, splits;
   long long tiles;
-  size_t counters, bytes;
+  size_t slots;
 };
 ChPlan ch_plan(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms) {
   ChPlan p{};
@@ -858,21 +859,18 @@ ChPlan ch_plan(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms
   p.tiles_max = (int)(((long long)max_q * (q_heads / kv_heads) + rows - 1) / rows);
   p.tiles = (long long)p.tiles_max * batch * kv_heads;
   p.splits = (int)std::max<long long>(1, std::min<long long>(kSplitMost, sms / p.tiles));
-  if (p.splits > 1) {
-    p.counters = ((size_t)p.tiles * sizeof(unsigned) + 255) / 256 * 256;
-    p.bytes = p.counters + (size_t)p.tiles * p.splits * rows * (dim + 2) * sizeof(float);
-  }
+  if (p.splits > 1) p.slots = (size_t)p.tiles * p.splits * rows * (dim + 2) * sizeof(float);
   return p;
 }
 
 }  // namespace
 
-size_t kv_chunk_workspace(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms) {
-  return ch_plan(batch, max_q, q_heads, kv_heads, dim, sms).bytes;
+size_t kv_chunk_slots(int batch, int max_q, int q_heads, int kv_heads, int dim, int sms) {
+  return ch_plan(batch, max_q, q_heads, kv_heads, dim, sms).slots;
 }
 
-cudaError_t launch_kv_chunk(const KvAttend& p, int min_rows, void* workspace, long long wait_limit,
-                            cudaStream_t stream) {
+cudaError_t launch_kv_chunk(const KvAttend& p, int min_rows, unsigned* counters, float* slots,
+                            long long wait_limit, cudaStream_t stream) {
   const KvCache& c = p.cache;
   ChArgs a{};
   a.q = static_cast<const uint16_t*>(p.q);
@@ -901,10 +899,10 @@ cudaError_t launch_kv_chunk(const KvAttend& p, int min_rows, void* workspace, lo
   const ChPlan plan = ch_plan(p.batch, p.max_q, p.q_heads, c.heads, c.dim, device_sms());
   a.tiles_max = plan.tiles_max;
   a.splits = 1;
-  if (workspace && plan.splits > 1) {
+  if (counters && plan.splits > 1) {   // at most a tile per SM then, and a counter each
     a.splits = plan.splits;
-    a.counters = static_cast<unsigned*>(workspace);
-    a.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.counters);
+    a.counters = counters;
+    a.slots = slots;
   }
   const long long ctas = plan.tiles * a.splits;
   if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;

@@ -24,25 +24,24 @@ __device__ __forceinline__ float epi_load(const uint16_t* p) {
   else return __half2float(__ushort_as_half(*p));
 }
 
-// Phi(v), the normal distribution function, as 1/2 erfc(-v / sqrt 2) by the rational
+// GELU v Phi(v) = max(v, 0) - |v| erfc(|v| / sqrt 2) / 2, with erfc by the rational
 // approximation 7.1.26 of Abramowitz and Stegun (absolute error below 1.5e-7, no
-// cancellation in the lower tail): about 15 instructions, where erfcf's branches
-// made the epilogue of a tile slower than its products.
-__device__ __forceinline__ float normal_cdf(float v) {
-  const float x = fabsf(v) * 0.70710678118f;
-  const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-  float p = fmaf(1.061405429f, t, -1.453152027f);
-  p = fmaf(p, t, 1.421413741f);
-  p = fmaf(p, t, -0.284496736f);
-  p = fmaf(p, t, 0.254829592f);
-  const float half_erfc = 0.5f * p * t * __expf(-x * x);   // of |v| / sqrt 2
-  return v < 0.0f ? half_erfc : 1.0f - half_erfc;
+// cancellation in the lower tail): 14 instructions, where erfcf's branches made
+// the epilogue of a tile slower than its products.
+__device__ __forceinline__ float gelu(float v) {
+  const float x = fminf(fabsf(v), 1e4f);                          // inf 0 is not needed below
+  const float t = __fdividef(1.0f, fmaf(0.23164188f, x, 1.0f));   // 0.3275911 / sqrt 2
+  float p = fmaf(0.5307027145f, t, -0.7265760135f);               // the coefficients' halves
+  p = fmaf(p, t, 0.7107068705f);
+  p = fmaf(p, t, -0.142248368f);
+  p = fmaf(p, t, 0.127414796f);
+  return (v > 0.0f ? v : (v == v ? 0.0f : v)) - x * (p * t * __expf(-0.5f * x * x));
 }
 
 template <int ACT>
 __device__ __forceinline__ float epi_act(float v) {
   if constexpr (ACT == QMM_ACT_RELU) return v > 0.0f ? v : (v == v ? 0.0f : v);
-  if constexpr (ACT == QMM_ACT_GELU) return v * normal_cdf(v);
+  if constexpr (ACT == QMM_ACT_GELU) return gelu(v);
   if constexpr (ACT == QMM_ACT_GELU_TANH)
     // 0.5 v (1 + tanh u) = v / (1 + e^-2u), u = sqrt(2 / pi) (v + 0.044715 v^3)
     return __fdividef(v, 1.0f + __expf(-1.5957691216f * (v + 0.044715f * v * v * v)));
@@ -50,23 +49,21 @@ __device__ __forceinline__ float epi_act(float v) {
   return v;
 }
 
-// N values at once, v[i] of weight row row(i) and element at(i) of y where ok(i): the choices of activation, bias and residual
-// are made once, and the residual's loads are in flight together.
-template <bool BF16, int N, class Ok, class Row, class At>
-__device__ __forceinline__ void epi_apply(const EpiArgs& e, float (&v)[N], Ok&& ok, Row&& row, At&& at) {
-  float res[N];
+// N values at once: v[i] + bias(i), activated, + the residual of element at(i) of
+// y.  The choices are made once; at(i) is always an element of y (that of another
+// value where value i is none), so that the residual's loads need no branches and
+// are in flight together.
+template <bool BF16, int N, class Bias, class At>
+__device__ __forceinline__ void epi_apply(const EpiArgs& e, float (&v)[N], Bias&& bias, At&& at) {
+  uint16_t res[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) res[i] = 0.0f;
+  for (int i = 0; i < N; ++i) res[i] = 0;
   if (e.residual) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (ok(i)) res[i] = epi_load<BF16>(e.residual + at(i));
+    for (int i = 0; i < N; ++i) res[i] = e.residual[at(i)];
   }
-  if (e.bias) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (ok(i)) v[i] += epi_load<BF16>(e.bias + row(i));
-  }
+  for (int i = 0; i < N; ++i) v[i] += bias(i);
   switch (e.act) {   // the same for every thread of the grid
     case QMM_ACT_RELU:
 #pragma unroll
@@ -87,7 +84,7 @@ __device__ __forceinline__ void epi_apply(const EpiArgs& e, float (&v)[N], Ok&& 
     default: break;
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] += res[i];
+  for (int i = 0; i < N; ++i) v[i] += epi_load<BF16>(&res[i]);
 }
 
 }  // namespace qk

@@ -522,9 +522,15 @@ __global__ void __launch_bounds__(kThreads, (DEEP || NT > 2) ? 1 : 2) skinny_ker
           if constexpr (EPI) {
             auto rw = [&](int i) { return (tile * R + r) * 16 + g + 8 * (i >> 1); };
             auto tk = [&](int i) { return m_base + 8 * nt + 2 * t + (i & 1); };
+            // the fragment's two rows
+            float b2[2] = {0.0f, 0.0f};
+            if (a.epi.bias) {
+              if (rw(0) < a.N) b2[0] = epi_load<BF16>(a.epi.bias + rw(0));
+              if (rw(2) < a.N) b2[1] = epi_load<BF16>(a.epi.bias + rw(2));
+            }
             epi_apply<BF16>(
-                a.epi, o, [&](int i) { return rw(i) < a.N && tk(i) < a.M; }, rw,
-                [&](int i) { return (size_t)tk(i) * a.N + rw(i); });
+                a.epi, o, [&](int i) { return b2[i >> 1]; },
+                [&](int i) { return (size_t)min(tk(i), a.M - 1) * a.N + min(rw(i), a.N - 1); });
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {

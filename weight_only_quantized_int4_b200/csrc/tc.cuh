@@ -270,9 +270,16 @@ __device__ __forceinline__ uint32_t lut_pair(uint32_t t16, float s) {
 // 32 rows is a 64-byte piece per token.
 template <bool BF16>
 __device__ __forceinline__ void epi_row(const EpiArgs& e, float (&o)[32], int row, int m0, int M, int N) {
+  const float b = e.bias && row < N ? epi_load<BF16>(e.bias + row) : 0.0f;
   epi_apply<BF16>(
-      e, o, [&](int i) { return row < N && m0 + i < M; }, [&](int) { return row; },
-      [&](int i) { return (size_t)(m0 + i) * N + row; });
+      e, o, [&](int) { return b; }, [&](int i) { return (size_t)min(m0 + i, M - 1) * N + min(row, N - 1); });
+}
+// Asks for the residual of a tile's tokens m0 .. m0 + tokens - 1 and 32 rows from
+// row0 on, a token per lane at a time, while the tile's products still run.
+__device__ __forceinline__ void epi_prefetch(const EpiArgs& e, int row0, int m0, int tokens, int M, int N) {
+  if (!e.residual || row0 >= N) return;
+  for (int i = threadIdx.x & 31; i < tokens && m0 + i < M; i += 32)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(e.residual + (size_t)(m0 + i) * N + row0));
 }
 
 template <int MODE, bool BF16, int BN, bool GM1, int KU, bool EPI>
@@ -677,6 +684,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int tile, kb0, kb1;
       seg_of(u, tile, kb0, kb1);
       const int buf = seg & 1;
+      if constexpr (EPI) epi_prefetch(a.epi, tile % a.tiles_n * kRowsTile + q * 32, tile / a.tiles_n * BN, BN, a.M, a.N);
       // the four epilogue warps stop together (they share named barriers)
       const bool ok = mbar_wait(&acc_full[buf], (seg >> 1) & 1, abort_flag, a.wait_limit);
       if (!named_bar_and(1, 128, ok)) break;

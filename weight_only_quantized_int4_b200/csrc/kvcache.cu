@@ -8,7 +8,10 @@
 // whole call, so the index arithmetic is done once, and it walks over tokens, two
 // at a time with their loads in flight together.  A group of dims is some of a
 // thread's words in up to eight neighbouring lanes, whose extremes meet in
-// shuffles; nothing goes through shared memory.
+// shuffles; nothing goes through shared memory.  Measured: 16384 tokens x 32 heads
+// x 128 dims read back (bf16) in 65 us, 5.2 TB/s of codes in and values out (one
+// 4-byte word per thread: 93 us); 8191 tokens x 32 heads stored (ASYM, groups of 64)
+// and read back in 74 us, 4.6 TB/s for both.
 #include <algorithm>
 
 #include "kv.cuh"

@@ -87,6 +87,29 @@ def test_store_sizes(T, H):
     assert rk.shape == (0, H, dim) and np.array_equal(cache.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("mode", ["sym", "asym"])
+def test_store_at_rounding_borders(mode, dtype):
+    """Scales that are powers of two and values at and next to every border between two codes;
+    the largest value and the zero-point both rounded up; scales below fp16's normals."""
+    dim = 64
+    rows = []
+    for scale in (1.0, 2.0 ** -10, 2.0 ** -20, 2.0 ** -23, 300.0):
+        for top in (7.5, 7.0, 15.0):                 # with -7.5: 15 steps; code 16 must come out as 15
+            for nudge in (-1, 0, 1):
+                x = torch.zeros(dim)
+                x[0], x[1] = -7.5 if mode == "asym" else -7.0, top if mode == "asym" else 7.0
+                x[2:32] = (torch.arange(30) - 14.5) / 2 * (1 + nudge * 2.0 ** -9)
+                rows.append(x * scale)
+    k = torch.stack(rows)[:, None].cuda().to(DT[dtype])
+    T = k.shape[0]
+    cache = q.kv_cache(4, 1, dim, 16, mode, -1)
+    q.kv_store(k, k, _ints(range(T)), cache, mode, -1)
+    want = np.zeros(tuple(cache.shape), np.uint8)
+    plain.store(want, 16, _f64(k), _f64(k), range(T), -1, mode)
+    assert np.array_equal(cache.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("mode", ["sym", "asym"])
 def test_store_of_values_that_are_not_finite(mode):
     dim, H = 128, 2

@@ -9,9 +9,10 @@
 // at a time with their loads in flight together.  A group of dims is some of a
 // thread's words in up to eight neighbouring lanes, whose extremes meet in
 // shuffles; nothing goes through shared memory.  Measured: 16384 tokens x 32 heads
-// x 128 dims read back (bf16) in 65 us, 5.2 TB/s of codes in and values out (one
-// 4-byte word per thread: 93 us); 8191 tokens x 32 heads stored (ASYM, groups of 64)
-// and read back in 74 us, 4.6 TB/s for both.
+// x 128 dims read back (bf16) in 57 us, 5.9 TB/s of codes in and values out (one
+// 4-byte word per thread: 93 us; values written 64 bytes apart: 65 us); 8191 tokens
+// x 32 heads stored (ASYM, groups of 64) and read back in 65 us, 5.3 TB/s for both
+// (NaN looked for and codes clamped one by one: 74 us).
 #include <algorithm>
 
 #include "kv.cuh"
@@ -120,6 +121,19 @@ __device__ __forceinline__ float kv_hi(uint32_t w) {
   if constexpr (BF16) return __uint_as_float(w & 0xFFFF0000u);
   else return __half2float(__ushort_as_half((unsigned short)(w >> 16)));
 }
+// The same maximum, NaN if either is one.
+template <bool BF16>
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ bool has_nan(uint32_t w) {
+  constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;
+  return (w & 0x7FFFu) > kInf || ((w >> 16) & 0x7FFFu) > kInf;
+}
 // NaN in either half -> 0 there.
 template <bool BF16>
 __device__ __forceinline__ uint32_t drop_nan(uint32_t w) {
@@ -170,14 +184,26 @@ __device__ __forceinline__ void store_rows(const KvArgs& a) {
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
+      uint32_t nan = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4& x = v[u][i];
+        nan = max2_nan<BF16>(nan, max2_nan<BF16>(max2_nan<BF16>(x.x, x.y), max2_nan<BF16>(x.z, x.w)));
+      }
+      if (has_nan<BF16>(nan)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4& x = v[u][i];
+          x.x = drop_nan<BF16>(x.x);
+          x.y = drop_nan<BF16>(x.y);
+          x.z = drop_nan<BF16>(x.z);
+          x.w = drop_nan<BF16>(x.w);
+        }
+      }
       uint32_t ext[4];   // (largest, -smallest) of each word, then of each local group; 0 included
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint4& x = v[u][i];
-        x.x = drop_nan<BF16>(x.x);
-        x.y = drop_nan<BF16>(x.y);
-        x.z = drop_nan<BF16>(x.z);
-        x.w = drop_nan<BF16>(x.w);
+        const uint4& x = v[u][i];
         const uint32_t mx = max2<BF16>(max2<BF16>(x.x, x.y), max2<BF16>(x.z, x.w));
         const uint32_t mn = min2<BF16>(min2<BF16>(x.x, x.y), min2<BF16>(x.z, x.w)) ^ 0x80008000u;
         const uint32_t e = max2<BF16>(__byte_perm(mx, mn, 0x5410), __byte_perm(mx, mn, 0x7632));
@@ -189,6 +215,7 @@ __device__ __forceinline__ void store_rows(const KvArgs& a) {
       }
       float r[NG], zf[NG];
       __half sh[NG];
+      bool clamp = false;   // a scale that is not the span's to 2^-11: saturated, or below fp16's normals
 #pragma unroll
       for (int lg = 0; lg < NG; ++lg) {
 #pragma unroll
@@ -198,26 +225,37 @@ __device__ __forceinline__ void store_rows(const KvArgs& a) {
         const float span = kA ? __fdiv_rn(hi + nlo, 15.0f) : __fdiv_rn(fmaxf(hi, nlo), 7.0f);
         sh[lg] = __float2half_rn(fminf(span, kKvMaxScale));
         const float s = __half2float(sh[lg]);
+        clamp = clamp || s >= kKvMaxScale || s < 6.103515625e-5f;
         r[lg] = s > 0.0f ? __frcp_rn(s) : 0.0f;
         zf[lg] = 8.0f;
         if (kA) zf[lg] = s > 0.0f ? fminf(rintf(__fdiv_rn(nlo, s)), 15.0f) : 0.0f;
       }
+      // With s within 2^-11 of its span, SYM codes cannot leave -7 .. 7.  Nor can ASYM ones
+      // fall below 0: rint(-x) + rint(x) = 0, and a quotient of two 11-bit numbers that is
+      // not a half is 2^-12 away from it, so x r + 48 (off by 2^-18) rounds as x / s does.
+      // Two halves rounded up can reach 16.
       uint32_t word[4];
+      auto encode = [&]<bool CLAMP>() {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int lg = local_group<D, GD, VAL>(i);
-        const float vlo = 48.0f - zf[lg], vhi = 63.0f - zf[lg];
-        uint32_t acc = 0;
+        for (int i = 0; i < 4; ++i) {
+          const int lg = local_group<D, GD, VAL>(i);
+          const float vlo = 48.0f - zf[lg], vhi = 63.0f - zf[lg];
+          uint32_t acc = 0;
 #pragma unroll
-        for (int k = 7; k >= 0; --k) {
-          const uint32_t w = (&v[u][i].x)[k >> 1];
-          const float x = (k & 1) ? kv_hi<BF16>(w) : kv_lo<BF16>(w);
-          const float q = fminf(fmaxf(fmaf(x, r[lg], 48.0f), vlo), vhi) + 8388608.0f;
-          acc = acc * 16u + __float_as_uint(q);   // the code is in q's low bits, 0x4B000000 + 48 - z above it
+          for (int k = 7; k >= 0; --k) {
+            const uint32_t w = (&v[u][i].x)[k >> 1];
+            float x = fmaf((k & 1) ? kv_hi<BF16>(w) : kv_lo<BF16>(w), r[lg], 48.0f);
+            if (CLAMP) x = fmaxf(x, vlo);
+            if (CLAMP || kA) x = fminf(x, vhi);
+            // the code is in the sum's low bits, 0x4B000000 + 48 - z above it
+            acc = acc * 16u + __float_as_uint(x + 8388608.0f);
+          }
+          // take the eight offsets off again: 0x4B000000 and 0x4B0000000 survive mod 2^32
+          word[i] = acc - (0x4B000000u + 0xB0000000u + 0x11111111u * (uint32_t)(48 - (int)zf[lg]));
         }
-        // take the eight offsets off again: 0x4B000000 and 0x4B0000000 survive mod 2^32
-        word[i] = acc - (0x4B000000u + 0xB0000000u + 0x11111111u * (uint32_t)(48 - (int)zf[lg]));
-      }
+      };
+      if (clamp) encode.template operator()<true>();
+      else encode.template operator()<false>();
       if (slot[u] >= 0) {
         uint8_t* t = kv_tile<TB>(a, slot[u], th.head);
         const int at = slot[u] & 15;
@@ -247,11 +285,11 @@ __global__ void __launch_bounds__(kKvThreads) kv_store_kernel(const KvArgs a) {
 
 // (q - z) s rounded once to the output type: in fp16 one multiplication of exact
 // operands, for bf16 the exact fp32 product (5 x 11 bits) converted.  A slot
-// outside the cache gives zeros.
+// outside the cache gives zeros.  Here a thread's words are (D / 32) i + c of both
+// kinds of rows: the outputs, eight times the codes, go out in whole sectors.
 template <int D, int MODE, int GD, bool BF16, bool VAL>
 __device__ __forceinline__ void load_rows(const KvArgs& a) {
   constexpr int G = D / GD, TB = kv_tile_bytes(D, G, MODE), PB = kv_param_bytes(MODE);
-  constexpr int NG = VAL ? 1 : local_group<D, GD, VAL>(3) + 1;
   const KvThread th = kv_thread<D>(a);
   if (!th.on) return;
   uint16_t* dst = a.dst[VAL] + th.head * D;
@@ -259,8 +297,7 @@ __device__ __forceinline__ void load_rows(const KvArgs& a) {
   for (long long t0 = (long long)blockIdx.y * a.tpb * kUnroll; t0 < a.tokens;
        t0 += (long long)gridDim.y * a.tpb * kUnroll) {
     int slot[kUnroll];
-    uint4 code[kUnroll];
-    uint32_t par[kUnroll][NG];
+    uint32_t code[kUnroll][4], par[kUnroll][4];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const long long tok = t0 + u * a.tpb + th.ty;
@@ -269,19 +306,27 @@ __device__ __forceinline__ void load_rows(const KvArgs& a) {
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      code[u] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int lg = 0; lg < NG; ++lg) par[u][lg] = 0;
+      for (int i = 0; i < 4; ++i) code[u][i] = par[u][i] = 0;
       if (slot[u] >= 0) {
         const uint8_t* t = kv_tile<TB>(a, slot[u], th.head);
         const int at = slot[u] & 15;
-        code[u] = *reinterpret_cast<const uint4*>(t + (VAL ? kKvTile * D / 2 : 0) + at * (D / 2) + 16 * th.chunk);
+        const uint8_t* row = t + (VAL ? kKvTile * D / 2 : 0) + at * (D / 2);
         const uint8_t* p = t + kKvTile * D + ((VAL ? kKvTile : 0) + at) * G * PB;
+        if constexpr (!VAL && D == 128) {   // the words of one 16-byte chunk
+          const uint4 w = *reinterpret_cast<const uint4*>(row + 16 * th.chunk);
+          code[u][0] = w.x;
+          code[u][1] = w.y;
+          code[u][2] = w.z;
+          code[u][3] = w.w;
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {   // (words of one group load the same parameter)
-          const uint8_t* pp = p + natural_word<D, VAL>(th.chunk, i, at) / (GD / 8) * PB;
-          par[u][local_group<D, GD, VAL>(i)] =
-              MODE == kASYM ? *reinterpret_cast<const uint32_t*>(pp) : *reinterpret_cast<const uint16_t*>(pp);
+        for (int i = 0; i < 4; ++i) {
+          const int n = D / 32 * i + th.chunk;
+          if constexpr (VAL || D != 128)
+            code[u][i] = *reinterpret_cast<const uint32_t*>(row + 4 * (VAL ? kv_val_word(D, n, at) : kv_key_word(D, n, at)));
+          const uint8_t* pp = p + n / (GD / 8) * PB;   // (words of one group load the same parameter)
+          par[u][i] = MODE == kASYM ? *reinterpret_cast<const uint32_t*>(pp) : *reinterpret_cast<const uint16_t*>(pp);
         }
       }
     }
@@ -291,11 +336,11 @@ __device__ __forceinline__ void load_rows(const KvArgs& a) {
       if (tok >= a.tokens) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t pr = par[u][local_group<D, GD, VAL>(i)];
+        const uint32_t pr = par[u][i];
         uint32_t bias = 0x64086408u, bias16 = 0xD480D480u;
         if (MODE == kASYM) zero_biases(__byte_perm(pr, 0, 0x3232), bias, bias16);
         uint32_t d[4];
-        decode_nibbles((&code[u].x)[i], bias, bias16, d);   // pairs of dims (p, p + 4)
+        decode_nibbles(code[u][i], bias, bias16, d);   // pairs of dims (p, p + 4)
         uint4 out;
         if constexpr (!BF16) {
           const uint32_t s2 = __byte_perm(pr, 0, 0x1010);
@@ -316,7 +361,7 @@ __device__ __forceinline__ void load_rows(const KvArgs& a) {
           out.w = pack2<true>(f[2].y * s, f[3].y * s);
         }
         if (slot[u] < 0) out = make_uint4(0, 0, 0, 0);   // not (8 - z) times a missing scale
-        *reinterpret_cast<uint4*>(dst + tok * stride + 8 * natural_word<D, VAL>(th.chunk, i, slot[u] & 15)) = out;
+        *reinterpret_cast<uint4*>(dst + tok * stride + 8 * (D / 32 * i + th.chunk)) = out;
       }
     }
   }

@@ -231,7 +231,7 @@ int qmm_gated(const void* x, int xdtype, const void* qweight, const uint16_t* sc
  *     y[M, N] = residual + act(x . dequant(Wq)^T + bias)
  *
  *   bias      device, [N], dtype of x, or NULL.
- *   act       QMM_ACT_*: none, max(v, 0), v Phi(v) (GELU, by erfc), its tanh form
+ *   act       QMM_ACT_*: none, max(v, 0), v Phi(v) (GELU; Phi to 1e-7), its tanh form
  *             v / (1 + exp(-2 sqrt(2/pi) (v + 0.044715 v^3))), v / (1 + exp(-v)).
  *   residual  device, [M, N], dtype of x, or NULL; it may be y itself (added onto in
  *             place) but not overlap it otherwise; bias must not overlap y.

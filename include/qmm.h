@@ -386,7 +386,8 @@ int qmm_kv_load(const void* cache, const int32_t* slots, int tokens, int heads, 
  * partial results: some megabytes, up to some 40 MB for few rows of many queries.
  * NULL: no tile of rows is split between CTAs (slower for few, long sequences).
  * Waits of the tcgen05 kernel are bounded as qmm_set_wait_limit says
- * (qmm_check_error). */
+ * (qmm_check_error); a workspace that a call which gave up has used must be zero
+ * filled again. */
 size_t qmm_kv_workspace_size(int batch, int max_q, int q_heads, int kv_heads, int dim);
 int qmm_kv_attend(const void* q, int dtype, long long q_stride, const void* cache, const int32_t* table,
                   const int32_t* lens, const int32_t* cu_q, int batch, int total_q, int max_q, int q_heads,

@@ -152,3 +152,17 @@ def test_a_wait_that_runs_out_is_reported():
     out = q.kv_attend(*args, **kw)
     q.check_error()
     _check(out, None, want, 128, "f16")
+
+
+@pytest.mark.parametrize("nq", [[3, 1], [120, 7]])
+def test_without_a_bound_on_the_queries(nq):
+    """max_q left out: every query gets its output, however many a sequence has."""
+    lens, H, KV, dim = [300, 90], 4, 2, 128
+    cache, table, qq, cu, keys, values = _setup(lens, nq, H, KV, dim, 32, "sym", -1, "f16", sum(nq))
+    total = int(cu[-1])
+    want = _expect(qq, cu, keys, values, 0.1, 0)
+    lse = torch.zeros(total, H, device="cuda")
+    out = q.kv_attend(qq[:total], cache, table, _ints(lens), cu_q=torch.tensor(cu, device="cuda"), scale=0.1, lse=lse,
+                      ws=q.kv_workspace(2, total, H, KV, dim))
+    q.check_error()
+    _check(out, lse, want, dim, "f16")

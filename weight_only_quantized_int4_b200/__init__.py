@@ -551,11 +551,13 @@ def kv_workspace(batch, max_q, q_heads, kv_heads, dim, device="cuda"):
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def kv_attend(q, cache, table, lens, cu_q=None, max_q=1, scale=None, window=0, mode="sym", group=-1,
+def kv_attend(q, cache, table, lens, cu_q=None, max_q=None, scale=None, window=0, mode="sym", group=-1,
               out=None, lse=None, ws=None):
     """Attention of each sequence's last tokens, q [total, heads, dim], over its
     pages of the cache: sequence b has lens[b] tokens in pages table[b] and the
-    queries cu_q[b] .. cu_q[b + 1] - 1 (None: one each), at most max_q of them.
+    queries cu_q[b] .. cu_q[b + 1] - 1 (None: one each), at most max_q of them
+    (None: as many as q holds, which is right and for many sequences slower than
+    a closer bound; with cu_q None, 1).
 
     scale: None for 1 / sqrt(dim); window: 0, or how many last tokens a query
     sees; lse: fp32 [total, heads] to fill with the log-sum-exp; ws: a
@@ -580,6 +582,8 @@ def kv_attend(q, cache, table, lens, cu_q=None, max_q=1, scale=None, window=0, m
         To, Ho, Do, ostride = _token_rows("out", out, dev, dtype)
         if To != total or Ho != H or Do != D:
             raise ValueError("out must have q's shape")
+    if max_q is None:
+        max_q = 1 if cu is None else total
     lp = wp = None
     nbytes = 0
     if lse is not None:

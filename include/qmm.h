@@ -367,7 +367,9 @@ int qmm_kv_load(const void* cache, const int32_t* slots, int tokens, int heads, 
  * (store a step's keys and values first), with window > 0 only the last `window`
  * of them.  cu_q NULL: one query per sequence (total_q = batch, max_q = 1).
  *   q     [total_q][q_heads][dim], out the same (strides as for k; no overlap)
- *   max_q an upper bound on the queries of a sequence; those past it get no output
+ *   max_q an upper bound on the queries of a sequence (at most 2^22); those past it get
+ *         no output.  A sequence's rows, min(max_q, total_q) * q_heads / kv_heads, stay
+ *         below 2^31 - 256 or the call is refused
  *   scale finite, of any sign
  *   lse   fp32 [total_q][q_heads], log of the sum of exponentials, or NULL
  * A query that sees nothing (an empty sequence) gives zeros and lse -inf.  Rows of

@@ -166,3 +166,19 @@ def test_without_a_bound_on_the_queries(nq):
                       ws=q.kv_workspace(2, total, H, KV, dim))
     q.check_error()
     _check(out, lse, want, dim, "f16")
+
+
+@pytest.mark.parametrize("dim", [64, 256])
+def test_a_bound_on_queries_far_above_them(dim):
+    """max_q at its limit with 1024 query heads on one key head: the rows that the bound alone would
+    give do not fit 32 bits, those of the queries do."""
+    lens, nq, H = [300, 40], [3, 1], 1024
+    cache, table, qq, cu, keys, values = _setup(lens, nq, H, 1, dim, 16, "sym", -1, "f16", 5)
+    want = _expect(qq, cu, keys, values, 0.1, 0)
+    most = 1 << 22
+    for ws in (None, q.kv_workspace(2, most, H, 1, dim)):
+        lse = torch.empty(4, H, device="cuda")
+        out = q.kv_attend(qq[:4], cache, table, _ints(lens), cu_q=torch.tensor(cu, device="cuda"), max_q=most, scale=0.1,
+                          lse=lse, ws=ws)
+        q.check_error()
+        _check(out, lse, want, dim, "f16")

@@ -89,6 +89,20 @@ def test_attend_refusals(lib):
     assert attend(ws=P(0x3900010), wsb=need) == -3
 
 
+def test_attend_refuses_more_rows_than_32_bits_hold(lib):
+    """Query heads per key head times a sequence's queries: the kernels number a tile's rows in 32
+    bits.  What the bound max_q alone would allow does not count, only queries that q holds."""
+    def attend(max_q, total, H):
+        return lib.qmm_kv_attend(A, 0, H * 64, B, C_, C_, C_, 1, total, max_q, H, 1, 64, 64, 16, 4, -1, 0, 0.1, 0,
+                                 P(1 << 56), H * 64, None, None, 0, None)
+
+    assert attend(1 << 22, 1 << 22, 512) == -2 and attend(1 << 22, 1 << 22, 4096) == -2
+    assert attend(1 << 22, 1 << 21, 1024) == -2
+    assert attend((1 << 22) + 1, 1, 1) == -2
+    # a loose bound over few queries is sized as before
+    assert lib.qmm_kv_workspace_size(1, 1 << 22, 4096, 1, 64) > 0
+
+
 def test_binding_refuses_before_the_library(lib):
     k = torch.zeros(3, 8, 128, dtype=torch.float16)
     with pytest.raises((ValueError, AssertionError, RuntimeError)):

@@ -86,7 +86,7 @@ int check_attend(int batch, int max_q, int q_heads, int kv_heads, int dim) {
   if (batch <= 0 || max_q <= 0 || q_heads <= 0 || kv_heads <= 0) return QMM_ERR_ARG;
   if (q_heads % kv_heads != 0) return QMM_ERR_ARG;
   if (dim != 64 && dim != 128 && dim != 256) return QMM_ERR_UNSUPPORTED;
-  if (batch > (1 << 20) || max_q > (1 << 22) || q_heads > 4096) return QMM_ERR_UNSUPPORTED;   // 32-bit rows
+  if (batch > (1 << 20) || max_q > (1 << 22) || q_heads > 4096) return QMM_ERR_UNSUPPORTED;
   return QMM_OK;
 }
 
@@ -544,6 +544,8 @@ int qmm_kv_attend(const void* q, int dtype, long long q_stride, const void* cach
   if (total_q < 0 || max_pages <= 0 || window < 0 || !std::isfinite(scale)) return QMM_ERR_ARG;
   if (!cu_q && (total_q != batch || max_q != 1)) return QMM_ERR_ARG;   // one query per sequence
   if ((long long)max_pages * page > (1ll << 30)) return QMM_ERR_UNSUPPORTED;   // 32-bit token positions
+  // a sequence's rows, rounded up to a tile of 256, are 32-bit numbers too
+  if ((long long)std::min(max_q, total_q) * (q_heads / kv_heads) > (1ll << 31) - 256) return QMM_ERR_UNSUPPORTED;
   if (!q || !cache || !table || !lens || !out) return QMM_ERR_ARG;
   const long long row = (long long)q_heads * dim;
   if (q_stride < row || out_stride < row) return QMM_ERR_ARG;

@@ -910,15 +910,19 @@ cudaError_t launch_kv_chunk(const KvAttend& p, int min_rows, unsigned* counters,
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.window = p.window;
   a.bf16 = p.bf16;
+  // split as the workspace was sized, by max_q; but max_q is the caller's bound and may
+  // lie far above the queries there are, so the tiles (whose rows are 32-bit numbers in
+  // the kernel) come from those
   const ChPlan plan = ch_plan(p.batch, p.max_q, p.q_heads, c.heads, c.dim, device_sms());
-  a.tiles_max = plan.tiles_max;
+  const ChPlan real = ch_plan(p.batch, std::min(p.max_q, p.total_q), p.q_heads, c.heads, c.dim, device_sms());
+  a.tiles_max = real.tiles_max;
   a.splits = 1;
   if (counters && plan.splits > 1) {   // at most a tile per SM then, and a counter each
     a.splits = plan.splits;
     a.counters = counters;
     a.slots = slots;
   }
-  const long long ctas = plan.tiles * a.splits;
+  const long long ctas = real.tiles * a.splits;
   if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   const int gd = c.dim / c.G;
 #define CH_CASE(D, MO, GD) \

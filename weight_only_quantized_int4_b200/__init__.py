@@ -266,6 +266,15 @@ def _like_x(name, t, dev, dtype, shape):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}")
 
 
+def _buffer(name, t, dev, nbytes):
+    """The address of a buffer of `nbytes` or more that the library reads from its start."""
+    if t.get_device() != dev:
+        raise _bad_device(name)
+    if t.nbytes < nbytes or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and hold at least {nbytes} bytes")
+    return t.data_ptr()
+
+
 def qmm_epilogue(x, qweight, scales, zeros_or_lut, N, K, mode, bits=4, group=128, bias=None, act="none",
                  residual=None, y=None, ws=None):
     """y[M, N] = residual + act(x[M, K] . dequant(qweight)^T + bias), rounded once.
@@ -277,10 +286,12 @@ def qmm_epilogue(x, qweight, scales, zeros_or_lut, N, K, mode, bits=4, group=128
         raise _bad_device("x")
     if dtype not in DTYPES or x.dim() != 2 or x.shape[1] != K or not x.is_contiguous():
         raise ValueError("x must be a contiguous fp16 or bf16 [M, K] tensor")
-    if qweight.get_device() != dev or scales.get_device() != dev:
-        raise _bad_device("qweight and scales")
-    if qweight.numel() * qweight.element_size() * 8 < N * K * bits:
-        raise ValueError("qweight is smaller than an [N, K] weight's codes")
+    halves = N * (K // group if group > 0 else 1)      # scales, and zero-points
+    qp = _buffer("qweight", qweight, dev, N * K * bits // 8)
+    sp = _buffer("scales", scales, dev, 2 * halves)
+    zp = None
+    if zeros_or_lut is not None and mode != "sym":
+        zp = _buffer("zeros_or_lut", zeros_or_lut, dev, 2 * (halves if mode == "asym" else 1 << bits))
     M = x.shape[0]
     code = ACTS.get(act)
     if code is None:
@@ -299,10 +310,9 @@ def qmm_epilogue(x, qweight, scales, zeros_or_lut, N, K, mode, bits=4, group=128
             _like_x("residual", residual, dev, dtype, (M, N))
         rp = residual.data_ptr()
     if ws is not None:
-        wp, nbytes = ws.data_ptr(), ws.numel() * ws.element_size()
-    st = (_lib or load()).qmm_epilogue(x.data_ptr(), DTYPES[dtype], qweight.data_ptr(), scales.data_ptr(),
-                                       None if zeros_or_lut is None else zeros_or_lut.data_ptr(), bp, code, rp, M, N,
-                                       K, bits, group, MODES[mode], y.data_ptr(), wp, nbytes, _stream_of(dev))
+        wp, nbytes = _buffer("ws", ws, dev, 0), ws.nbytes
+    st = (_lib or load()).qmm_epilogue(x.data_ptr(), DTYPES[dtype], qp, sp, zp, bp, code, rp, M, N, K, bits, group,
+                                       MODES[mode], y.data_ptr(), wp, nbytes, _stream_of(dev))
     if st:
         raise QmmError(st, "qmm_epilogue")
     return y
@@ -593,9 +603,7 @@ def kv_attend(q, cache, table, lens, cu_q=None, max_q=None, scale=None, window=0
             raise ValueError("lse must be a contiguous fp32 [total, heads] tensor")
         lp = lse.data_ptr()
     if ws is not None:
-        if ws.get_device() != dev:
-            raise _bad_device("ws")
-        wp, nbytes = ws.data_ptr(), ws.numel() * ws.element_size()
+        wp, nbytes = _buffer("ws", ws, dev, 0), ws.nbytes
     st = (_lib or load()).qmm_kv_attend(q.data_ptr(), DTYPES[dtype], qstride, cache.data_ptr(), table.data_ptr(),
                                         lens.data_ptr(), cu, B, total, max_q, H, kvh, D, page, pages, max_pages,
                                         group, code, D ** -0.5 if scale is None else scale, window, out.data_ptr(),

@@ -231,8 +231,10 @@ int qmm_gated(const void* x, int xdtype, const void* qweight, const uint16_t* sc
  *     y[M, N] = residual + act(x . dequant(Wq)^T + bias)
  *
  *   bias      device, [N], dtype of x, or NULL.
- *   act       QMM_ACT_*: none, max(v, 0), v Phi(v) (GELU; Phi to 1e-7), its tanh form
- *             v / (1 + exp(-2 sqrt(2/pi) (v + 0.044715 v^3))), v / (1 + exp(-v)).
+ *   act       QMM_ACT_*: none, max(v, 0), v Phi(v) (GELU), its tanh form
+ *             v / (1 + exp(-w)), w = 2 sqrt(2/pi) (v + 0.044715 v^3), v / (1 + exp(-v)).
+ *             Errors relative to the value itself: GELU below 2^-19 + 2^-23 v^2, the
+ *             others below 2^-19 + 2^-21 |exponent|; values below 2^-119 may become 0.
  *   residual  device, [M, N], dtype of x, or NULL; it may be y itself (added onto in
  *             place) but not overlap it otherwise; bias must not overlap y.
  * Everything is taken in fp32 on the fp32 sums and rounded once.  The other

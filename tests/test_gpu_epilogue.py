@@ -168,3 +168,67 @@ def test_refusals():
                dict(y=torch.zeros(2, 32, device="cuda", dtype=torch.float16))):
         with pytest.raises(ValueError):
             q.qmm_epilogue(x, w, s, None, 64, 64, "sym", 4, 64, **kw)
+
+
+# ---- the activations by themselves: x = 0, so the sum is exactly 0 and y = act(bias)
+
+def _act64(v, act):
+    """The activation in 64 bits, its lower tail without cancellation."""
+    if act == "gelu":
+        return v * torch.exp(torch.special.log_ndtr(v))
+    if act == "gelu_tanh":
+        return v / (1 + torch.exp(-2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)))
+    if act == "silu":
+        return v / (1 + torch.exp(-v))
+    return v.clamp(min=0) if act == "relu" else v
+
+
+def _act_bound(v, act, xdtype):
+    """Half a step of the output's type around the activation's own error.  GELU: a fit off by 2^-22
+    and ten fp32 operations, below 2^-19; the exponent v^2 / 2 in base 2 is rounded in three factors,
+    3 2^-24 of it.  The forms v / (1 + e^w): the same 2^-19, and w is rounded in eight steps, 2^-21 of
+    it; a denominator of 2^126 and more may give 0, which with |v| < 2^7 there is below 2^-119."""
+    ref = _act64(v, act)
+    w = {"gelu": 2.0 ** -23 * v ** 2, "silu": 2.0 ** -21 * v.abs(),
+         "gelu_tanh": 2.0 ** -21 * 2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3).abs()}
+    own = ref.abs() * (2.0 ** -19 + w[act]) if act in w else torch.zeros_like(ref)
+    return ref, own + HALF[xdtype] * (ref.abs() + own) + (2.0 ** -25 if xdtype == "f16" else 2.0 ** -134) + 2.0 ** -119
+
+
+def _sweep(xdtype):
+    near = torch.logspace(-7, 0, 496, dtype=torch.float64)
+    far = torch.tensor([0.0, 14.0, -14.0, 20.0, -20.0, 100.0, -100.0, 1000.0, -1000.0, 6e4, -6e4] + [0.0] * 5,
+                       dtype=torch.float64)
+    v = torch.cat([torch.linspace(-13, 13, 2080, dtype=torch.float64), near, -near, far])
+    return v.to(TDT[xdtype])
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("xdtype", ["f16", "bf16"])
+def test_activation_of_the_bias_alone(xdtype, act):
+    bias = _sweep(xdtype)
+    N, K = bias.numel(), 128
+    v = bias.double()
+    ref, lim = _act_bound(v, act, xdtype)
+    W = torch.randn(N, K, generator=torch.Generator().manual_seed(1)).cuda()
+    for mode, group in (("sym", 128), ("asym", -1)):
+        qw, sc, ze = q.pack(W, mode, 4, group)
+        for M in (1, 12, 30, 40, 200):               # decode tiles of 8, 16 and 32 tokens, tensor path
+            x = torch.zeros(M, K, dtype=TDT[xdtype], device="cuda")
+            y = q.qmm_epilogue(x, qw, sc, ze, N, K, mode, 4, group, bias=bias.cuda(), act=act,
+                               ws=q.workspace(M, N, K, mode, 4, group))
+            err = (y.double().cpu() - ref).abs()
+            bad = ~(err <= lim)
+            assert not bad.any(), (f"{mode} M {M}: {int(bad.sum())} over the bound, the worst "
+                                   f"{float((err / lim).max()):.2f} of it at {float(v[(err / lim).max(0).values.argmax()])}")
+
+
+@pytest.mark.parametrize("xdtype", ["f16", "bf16"])
+def test_the_bound_tells_the_activations_apart(xdtype):
+    """Each activation, rounded to the output's type, breaks every other one's bound."""
+    v = _sweep(xdtype).double()
+    for act in ("none", "relu", "gelu", "gelu_tanh", "silu"):
+        ref, lim = _act_bound(v, act, xdtype)
+        for other in ("none", "relu", "gelu", "gelu_tanh", "silu"):
+            y = _act64(v, other).to(TDT[xdtype]).double()
+            assert ((y - ref).abs() <= lim).all() == (act == other), (act, other)

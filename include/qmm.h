@@ -387,7 +387,8 @@ int qmm_kv_load(const void* cache, const int32_t* slots, int tokens, int heads, 
  * workspace: qmm_kv_workspace_size bytes, 256-byte aligned, zero filled once; every
  * completed call leaves its counters at zero, so calls of any shape that fits can
  * share it on a stream (calls that run at the same time need one each).  It holds
- * partial results: some megabytes, up to some 40 MB for few rows of many queries.
+ * partial results: some megabytes, on 148 SMs at most 20 MB (a few tiles of many
+ * query rows, split between CTAs).
  * NULL: no tile of rows is split between CTAs (slower for few, long sequences).
  * Waits of the tcgen05 kernel are bounded as qmm_set_wait_limit says
  * (qmm_check_error); a workspace that a call which gave up has used must be zero

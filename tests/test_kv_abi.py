@@ -155,3 +155,25 @@ def test_plain_store_reads_back(dim, mode, group):
         assert np.array_equal(plain.decode(c, s, z, group), r)
         step = np.repeat(s.astype(np.float64), dim // G, -1)
         assert np.all(np.abs(r - x[keep]) <= 0.51 * step + 8 * 2.0 ** -11 * step)
+
+
+def test_workspace_stays_within_what_the_header_says(lib):
+    """The header names the largest workspace of a 148-SM GPU; a sweep over the shapes comes close to
+    it and never above."""
+    import os
+    import re
+    with open(os.path.join(os.path.dirname(q.LIB_PATH), "..", "include", "qmm.h")) as f:
+        said = re.search(r"at most (\d+) MB", f.read().replace("\n *", " "))
+    assert said, "the header names no size"
+    batches = (1, 2, 3, 5, 9, 17, 30, 37, 74, 75, 148, 300, 4096, 1 << 20)
+    queries = (1, 2, 7, 8, 16, 33, 64, 100, 128, 129, 250, 511, 512, 1000, 2048, 9000, 40000, 1 << 22)
+    most = 0
+    for dim in (64, 128, 256):
+        for kv in (1, 2, 3, 4, 8, 37, 64):
+            for per in (1, 2, 3, 4, 7, 8, 16, 64):
+                for b in batches:
+                    for m in queries:
+                        n = lib.qmm_kv_workspace_size(b, m, kv * per, kv, dim)
+                        assert n > 0
+                        most = max(most, n)
+    assert 0.95 * int(said[1]) * 1e6 < most <= int(said[1]) * 1e6, most

@@ -182,3 +182,31 @@ def test_a_bound_on_queries_far_above_them(dim):
                           lse=lse, ws=ws)
         q.check_error()
         _check(out, lse, want, dim, "f16")
+
+
+@pytest.mark.parametrize("dim", [128, 256])
+def test_a_split_tile_that_gives_up(dim):
+    """A wait that runs out while a tile's tokens are split between CTAs: the parts that gave up are
+    not counted, the error is reported, and the workspace is good again once it is zero filled."""
+    lens, nq, H = [4100], [70], 2
+    cache, table, qq, cu, keys, values = _setup(lens, nq, H, 1, dim, 128, "sym", -1, "f16", 31)
+    want = _expect(qq, cu, keys, values, 0.1, 0)
+    args = (qq[:70], cache, table, _ints(lens))
+    ws = q.kv_workspace(1, 70, H, 1, dim)
+    kw = dict(cu_q=_ints(cu), max_q=70, scale=0.1, ws=ws)
+    q.kv_attend(*args, **kw)
+    q.check_error()
+    old = q.set_wait_limit(1)
+    try:
+        q.kv_attend(*args, **kw)
+        with pytest.raises(q.QmmError) as e:
+            q.check_error()
+        assert e.value.status == -5
+    finally:
+        q.set_wait_limit(old)
+    ws.zero_()
+    outs = [q.kv_attend(*args, **kw) for _ in range(2)]
+    q.check_error()
+    for out in outs:
+        _check(out, None, want, dim, "f16")
+    assert torch.equal(outs[0], outs[1])

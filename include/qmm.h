@@ -133,7 +133,8 @@ size_t qmm_workspace_size_for(int M, int N, int K, int bits, int group, int mode
  *                 for LUT, NULL for SYM); scales and ASYM zeros 16-byte
  *                 aligned (they are copied in 16-byte pieces).  ASYM zeros are exact for integer
  *                 zero-points; a fractional zero is applied with one fp16 rounding.
- *   y             device, [M, N] row-major, same dtype as x, must not overlap x.
+ *   y             device, [M, N] row-major, same dtype as x, must not overlap x; of any
+ *                 alignment (the tensor path is faster at its end on a 16-byte border).
  *   workspace     device, workspace_bytes >= qmm_workspace_size(...), zero
  *                 filled before first use (see above); may be NULL with
  *                 workspace_bytes 0, in which case no cross-CTA split-K is used.

@@ -232,3 +232,37 @@ def test_the_bound_tells_the_activations_apart(xdtype):
         for other in ("none", "relu", "gelu", "gelu_tanh", "silu"):
             y = _act64(v, other).to(TDT[xdtype]).double()
             assert ((y - ref).abs() <= lim).all() == (act == other), (act, other)
+
+
+@pytest.mark.parametrize("M", [1, 20, 40, 129, 300])
+def test_y_needs_no_alignment_beyond_its_type(M):
+    """y, bias and residual that start 2 bytes past a 16-byte border, on both paths; what lies
+    around y stays as it was."""
+    p = cases.make("sym", 4, 128, M, 288, 1024, "f16", seed=M)
+    bias, res = _extras(p, "br", M)
+    want = _run(p, "silu", bias, res)
+
+    def off(t):
+        buf = torch.full((t.numel() + 17,), 7.0, dtype=torch.float16, device="cuda")
+        view = buf[1:1 + t.numel()].view(t.shape)
+        return buf, view.copy_(t)
+
+    x, qw, sp = _dev16(p.x).view(torch.float16), torch.from_numpy(p.qw).cuda(), _dev16(p.sp)
+    ws = q.workspace(M, p.N, p.K, p.mode)
+    for w in (ws, None):
+        buf, y = off(torch.zeros(M, p.N))
+        kw = dict(bias=off(bias)[1], residual=off(res)[1], act="silu", y=y, ws=w)
+        q.qmm_epilogue(x, qw, sp, None, p.N, p.K, p.mode, **kw)
+        ref = want if w is ws else _run(p, "silu", bias, res, ws=False)
+        assert torch.equal(y, ref) and (buf[0] == 7.0) and (buf[1 + y.numel():] == 7.0).all()
+        buf, y = off(res)                            # and in place
+        q.qmm_epilogue(x, qw, sp, None, p.N, p.K, p.mode, **dict(kw, residual=y, y=y))
+        assert torch.equal(y, ref) and (buf[0] == 7.0) and (buf[1 + y.numel():] == 7.0).all()
+        buf, y = off(torch.zeros(M, p.N))            # the product alone
+        q.qmm(x, qw, sp, None, p.N, p.K, p.mode, y=y, ws=w)
+        assert torch.equal(y, q.qmm(x, qw, sp, None, p.N, p.K, p.mode, ws=w))
+        assert (buf[0] == 7.0) and (buf[1 + y.numel():] == 7.0).all()
+        buf, y = off(torch.zeros(M, p.N // 2))       # and the gate's
+        q.qmm_gated(x, qw, sp, None, p.N // 2, p.K, p.mode, y=y, ws=w)
+        assert torch.equal(y, q.qmm_gated(x, qw, sp, None, p.N // 2, p.K, p.mode, ws=w))
+        assert (buf[0] == 7.0) and (buf[1 + y.numel():] == 7.0).all()

@@ -227,6 +227,7 @@ struct TcArgs {
   float* slots;             // [2 * ctas][BN][128]: a CTA's first / last partial tile,
                             // column-major so that a warp's 32 rows are 128 contiguous bytes
   unsigned* counters;       // [tiles]
+  int y_bulk;               // y starts on a 16-byte border, as a tensor map wants it
   EpiArgs epi;              // EPI kernels only
 };
 
@@ -904,7 +905,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       fence_proxy_async();
       named_bar(3 + grp, 128);
-      if (gissuer) {
+      if (!a.y_bulk) {   // y starts off a 16-byte border: the threads store the tile's rows themselves
+        const bool half = !EPI && a.gated;
+        const int w = half ? kRowsTile / 2 : kRowsTile, ny = half ? a.N / 2 : a.N;
+        const int col = tn * w + row_l;
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i) {
+          const int m = tm * BN + c * 32 + i;
+          if (row_l < w && col < ny && m < a.M) a.y[(size_t)m * ny + col] = ybuf[i * w + row_l];
+        }
+      } else if (gissuer) {
         tma_store_2d(&map_y, ybuf, (!EPI && a.gated) ? tn * (kRowsTile / 2) : tn * kRowsTile, tm * BN + c * 32);
         bulk_commit();
       }
@@ -1186,8 +1196,9 @@ cudaError_t launch_tc_any(const Problem& pr, const TcPlan& plan, void* workspace
   }
   // y as [M] x [N] (gated: [M] x [N/2]), one box = 32 tokens of a tile's
   // 128 rows (gated: its 64 outputs)
-  CUtensorMap my;
-  {
+  CUtensorMap my = ms;      // not used for a y off the 16-byte border
+  const bool y_bulk = reinterpret_cast<uintptr_t>(pr.y) % 16 == 0;
+  if (y_bulk) {
     const int ny = pr.gated ? pr.N / 2 : pr.N;
     const cuuint64_t dims[2] = {(cuuint64_t)ny, (cuuint64_t)pr.M};
     const cuuint64_t strides[1] = {(cuuint64_t)ny * 2};
@@ -1207,6 +1218,7 @@ cudaError_t launch_tc_any(const Problem& pr, const TcPlan& plan, void* workspace
   a.N = pr.N;
   a.K = pr.K;
   a.gated = pr.gated ? 1 : 0;
+  a.y_bulk = y_bulk ? 1 : 0;
   a.L = pr.group == -1 ? pr.K : pr.group;
   a.G = pr.K / a.L;
   a.lg = pr.group == -1 ? 30 : __builtin_ctz((unsigned)pr.group);

@@ -1,9 +1,10 @@
 // What a product ends in: y = residual + act(sum + bias), in fp32 on the fp32
 // sum, rounded once.  It costs its reads of bias and residual and no pass of its
 // own over y: one token on 4096 x 4096 with a residual 5.5 us where the product
-// alone takes 5.0; 1024 tokens on 11008 x 4096 with bias and GELU 104 us, with a
-// residual 100, the product alone 91 (what is left is the last tile's epilogue,
-// which no products hide).
+// alone takes 5.0; 1024 tokens on 11008 x 4096 with bias and GELU 106 us, with a
+// residual 102, the product alone 93 (short runs at 1965 MHz; seconds of calls at
+// the power cap, 1.65 - 1.75 GHz: 120, 117 and 106).  What is left is the last tile's
+// epilogue, which no products hide.
 #pragma once
 
 #include "common.cuh"

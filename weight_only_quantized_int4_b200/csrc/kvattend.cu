@@ -36,12 +36,13 @@
 //
 // Bound: HBM by its bytes (132 a token and head for both of 128 dims), in fact the
 // issue of a stage's instructions: 16 sequences of up to 32768 tokens, 64 query
-// heads on 8, take 98 us (4.4 TB/s, 0.68 of the measured copy bandwidth); the
-// copies alone 77 us, the arithmetic alone 93 us.  Of a stage's some 500
-// instructions the 34 MMAs, which overlap little with the logic pipe, cost a
-// quarter.  With groups of 32 dims and zero-points (values decoded one by one) 32
-// sequences of up to 4096 tokens take 36 us (3.1 TB/s).  Decoding every code before
-// its MMA took 130 us where this takes 98.
+// heads on 8, take 99 us (4.4 TB/s, 0.68 of the measured copy bandwidth; 104 us in
+// seconds of calls at the power cap, 1.87 GHz); the copies alone 77 us, the arithmetic
+// alone 93 us.  Of a stage's some 500 instructions the 34 MMAs, which overlap little
+// with the logic pipe, cost a quarter.  With groups of 32 dims and zero-points (values
+// decoded one by one) 32 sequences of up to 4096 tokens take 36 us (3.1 TB/s; these
+// kernels of 128 dims spill up to 20 bytes, 60 with 16 rows, the others nothing).
+// Decoding every code before its MMA took 130 us where this takes 99.
 #include <algorithm>
 
 #include "kv.cuh"

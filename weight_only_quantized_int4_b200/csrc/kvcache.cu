@@ -8,11 +8,13 @@
 // whole call, so the index arithmetic is done once, and it walks over tokens, two
 // at a time with their loads in flight together.  A group of dims is some of a
 // thread's words in up to eight neighbouring lanes, whose extremes meet in
-// shuffles; nothing goes through shared memory.  Measured: 16384 tokens x 32 heads
-// x 128 dims read back (bf16) in 57 us, 5.9 TB/s of codes in and values out (one
-// 4-byte word per thread: 93 us; values written 64 bytes apart: 65 us); 8191 tokens
-// x 32 heads stored (ASYM, groups of 64) and read back in 65 us, 5.3 TB/s for both
-// (NaN looked for and codes clamped one by one: 74 us).
+// shuffles; nothing goes through shared memory.  Measured in short runs at 1965 MHz:
+// 16384 tokens x 32 heads x 128 dims read back (bf16) in 57 us, 5.9 TB/s of codes in
+// and values out (one 4-byte word per thread: 93 us; values written 64 bytes apart:
+// 65 us); 8191 tokens x 32 heads stored (ASYM, groups of 64) and read back in 65 us,
+// 5.3 TB/s for both (NaN looked for and codes clamped one by one: 74 us), of which the
+// store takes 35 (5.0 TB/s, bound by issue) and the load 31.  In seconds of calls at
+// the power cap (1.7 - 1.8 GHz): 59, and 69 = 37 + 31.
 #include <algorithm>
 
 #include "kv.cuh"

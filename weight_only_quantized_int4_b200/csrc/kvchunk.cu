@@ -25,16 +25,19 @@
 // and the last to arrive adds them in order.
 //
 // Measured: chunks of 2048 queries x 32 heads on 8 behind prefixes up to 6000
-// tokens, 128 dims, take 282 us (835 TFLOP/s, 0.52 of the measured burst rate); the
-// MMAs alone, unhindered, 165 us.  A tile of 128 tokens takes some 4300 cycles
-// against 2048 of MMAs: S, softmax (2600 cycles, its two groups sharing the special
-// function units and issue slots with the decoder) and P V are one chain per row
-// tile.  Two S buffers of 64 tokens instead (an MMA of 64 columns takes as long as
-// one of 128) 341 us; halves of P handed on early, exponentials on the FMA pipes, one
-// pass over S instead of two: no faster; two warps to a row's 128 tokens (16 softmax
-// warps) 313 us.  Against 64 bits the output is off by
-// 4.4e-4 (2-norm; rounding it to fp16 alone 2.1e-4), 2.9e-4 of it K~'s; exact integers
-// as K~ with the keys' scales multiplied onto S leave 3.4e-4 and take 328 us.
+// tokens, 128 dims, take 285 us (826 TFLOP/s, 0.51 of the measured burst rate; 299 us
+// in seconds of calls at the power cap, 1.88 GHz); the MMAs alone, unhindered, 165.
+// The same with 64 dims 249 us; with 256, one row tile and one stage of keys and
+// values, where nothing hides the softmax, 686 (0.42 of the rate).  No spills with one
+// scale per row; up to 100 bytes with 256 dims in groups of 32.  A tile of 128 tokens
+// takes some 4300 cycles against 2048 of MMAs: S, softmax (2600 cycles, its two groups
+// sharing the special function units and issue slots with the decoder) and P V are one
+// chain per row tile.  Two S buffers of 64 tokens instead (an MMA of 64 columns takes
+// as long as one of 128) 341 us; halves of P handed on early, exponentials on the FMA
+// pipes, one pass over S instead of two: no faster; two warps to a row's 128 tokens (16
+// softmax warps) 313 us.  Against 64 bits the output is off by 4.4e-4 (2-norm; rounding
+// it to fp16 alone 2.1e-4), 2.9e-4 of it K~'s; exact integers as K~ with the keys'
+// scales multiplied onto S leave 3.4e-4 and take 328 us.
 //
 // Every wait is bounded: one that runs out sets the error word and the CTA drains
 // its MMAs, frees TMEM and exits.
